@@ -69,7 +69,8 @@ enum moe_status {
 };
 
 enum moe_act { MOE_ACT_SWIGLU = 0, MOE_ACT_GEGLU = 1 };
-enum moe_wfmt { MOE_WFMT_BF16 = 0, MOE_WFMT_INT4_G128 = 1 };
+enum moe_wfmt { MOE_WFMT_BF16 = 0, MOE_WFMT_INT4_G128 = 1, MOE_WFMT_INT8 = 2 };
+enum moe_dtype { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 };
 
 /*
  * Layer shape.
@@ -106,6 +107,9 @@ typedef struct moe_shape {
  *                       nibbles, input index 2i in the low nibble of byte i;
  *                       s13 [E, 2H, d/128] bf16, s2 [E, d, H/128] bf16: one scale per
  *                       128 consecutive inputs of an output row; weight = q * s.
+ *   MOE_WFMT_INT8:      w13 [E, 2H, d] int8, w2 [E, d, H] int8; s13 [E, 2H] fp32, s2 [E, d] fp32: one scale per
+ *                       output channel; weight = q * s (moe_quantize_int8 makes both from the rows of a weight).
+ *                       The products run in 8-bit integers on both sides: see moe_expert_ffn_int8.
  * The shared expert uses the same layouts with E = 1 and H = H_s.
  */
 
@@ -192,6 +196,7 @@ int moe_permute(const moe_shape* s, const void* x, const int32_t* topk_idx, int3
  *                                         MOE_INVALID_ARGUMENT)
  *   y             [R, d] bf16             out  rows outside every group are untouched
  * Accumulation is fp32; h is rounded to bf16 once, y once (the same values with h NULL or not).
+ * bf16 and INT4 experts; MOE_WFMT_INT8 gives MOE_INVALID_ARGUMENT (moe_expert_ffn_int8 has the scratch it needs).
  */
 int moe_expert_ffn(const moe_shape* s, int32_t n_groups, int32_t hidden, int64_t R, const void* x_grouped,
                    const int32_t* group_start, const int32_t* group_rows, const void* w13, const void* s13,
@@ -211,6 +216,77 @@ int moe_combine(const moe_shape* s, const void* y_perm, const int32_t* slot_pos,
                 const void* y_shared, void* out, moe_stream_t stream);
 
 /*
+ * Symmetric 8-bit quantisation of rows with one scale a row: the tokens of the 8-bit integer experts, and their
+ * weights' output channels (any leading dimensions, rows = their product).  With m = max|x_r|:
+ *   s_r = m / 127,  q = rint(127 x / m) (ties to even; -127 .. 127).
+ * For bf16 rows q is that value exactly; for fp32 rows a quotient within 2^-16 of a tie may go either way.  A row
+ * with m < 2^-119 gets s = 0 and q = 0.  A row that holds an infinity or a NaN gets it as its scale.
+ *   x      [rows, K] bf16 or fp32 (dtype, enum moe_dtype)   in    K a multiple of 16
+ *   q      [rows, K] int8                                   out
+ *   scales [rows] fp32                                      out
+ */
+int moe_quantize_int8(const void* x, int32_t dtype, int64_t rows, int32_t K, int8_t* q, float* scales,
+                      moe_stream_t stream);
+
+/*
+ * moe_permute with the rows quantised on the way (moe_quantize_int8 of x[t]): each token is read and quantised once,
+ * and its codes and scale written to the row of each kept slot.
+ *   xq_perm [R, d] int8   out,  xs_perm [R] fp32   out   unfilled rows untouched
+ * Other arguments, rules and errors as moe_permute (any wfmt).
+ */
+int moe_permute_int8(const moe_shape* s, const void* x, const int32_t* topk_idx, int32_t* slot_pos,
+                     uint8_t* drop_mask, int32_t* counts, int32_t* kept, int32_t* offsets, int32_t* row_src,
+                     int8_t* xq_perm, float* xs_perm, void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* Scratch bytes moe_expert_ffn_int8 needs for R rows of experts of this hidden width. */
+int moe_expert_ffn_int8_workspace_size(const moe_shape* s, int32_t hidden, int64_t R, size_t* bytes);
+
+/*
+ * Grouped gated expert FFN in 8-bit integers with scales for each token and each channel (s->wfmt MOE_WFMT_INT8).
+ * For a row r of group g with codes x_r and scale xs_r:
+ *   g = (x_r W1^T) xs_r s1,  u = (x_r W3^T) xs_r s3     exact 32-bit integer sums, scaled in fp32
+ *   h = act(g) u, rounded to bf16;  (hq, hs) = moe_quantize_int8(h)
+ *   y = (hq W2^T) hs s2, rounded to bf16
+ *   n_groups, hidden, R, group_start, group_rows   as moe_expert_ffn (groups are clipped to the R rows)
+ *   xq [R, d] int8, xs [R] fp32      in   moe_permute_int8, or moe_quantize_int8 of grouped rows
+ *   w13, s13, w2, s2                 in   n_groups experts, MOE_WFMT_INT8 layout
+ *   y  [R, d] bf16                   out  rows outside every group are untouched
+ *   workspace  >= moe_expert_ffn_int8_workspace_size() bytes, 256-byte aligned
+ */
+int moe_expert_ffn_int8(const moe_shape* s, int32_t n_groups, int32_t hidden, int64_t R, const int8_t* xq,
+                        const float* xs, const int32_t* group_start, const int32_t* group_rows, const int8_t* w13,
+                        const float* s13, const int8_t* w2, const float* s2, void* y, void* workspace,
+                        size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Gradient of moe_combine, for experts of the caller's own between moe_permute and moe_combine (moe_backward holds
+ * it for this library's experts).  The gradient of y_shared is dout itself.
+ *   dout     [T, d] bf16        in
+ *   y_perm   [R, d] bf16        in   the rows moe_combine read (may be NULL without dtopk_w)
+ *   slot_pos [T, k] int32       in   -1 = dropped (any value outside [0, R) counts as dropped); no row twice
+ *   topk_w   [T, k] fp32        in
+ *   kept     [E] int32 or NULL  in   with a capacity: rows filled in each group; the rows behind them are zeroed in
+ *                                    dy_perm (NULL: rows that no slot fills are untouched)
+ *   dy_perm  [R, d] bf16 / NULL out  dy_perm[slot_pos[t,j]] = topk_w[t,j] dout_t, one rounding
+ *   dtopk_w  [T, k] fp32 / NULL out  <dout_t, y_perm[slot_pos[t,j]]> in fp32, 0 where dropped
+ * Deterministic.  Errors: MOE_INVALID_ARGUMENT when both outputs are NULL, or kept without a capacity or dy_perm.
+ */
+int moe_combine_backward(const moe_shape* s, const void* dout, const void* y_perm, const int32_t* slot_pos,
+                         const float* topk_w, const int32_t* kept, void* dy_perm, float* dtopk_w,
+                         moe_stream_t stream);
+
+/*
+ * Gradient of the row moves of moe_permute: dx_t = sum over the token's kept slots of dx_perm[slot_pos[t,j]]
+ * (+ add_t), summed in fp32 in slot order, rounded once.
+ *   dx_perm  [R, d] bf16 or fp32 (in_dtype, enum moe_dtype)    in
+ *   slot_pos [T, k] int32                                      in   outside [0, R): dropped, contributes nothing
+ *   add      [T, d] out_dtype, or NULL                         in   may be dx itself (accumulation)
+ *   dx       [T, d] bf16 or fp32 (out_dtype)                   out
+ */
+int moe_permute_backward(const moe_shape* s, const void* dx_perm, int32_t in_dtype, const int32_t* slot_pos,
+                         const void* add, void* dx, int32_t out_dtype, moe_stream_t stream);
+
+/*
  * The whole layer: route -> permute -> grouped FFN -> shared expert -> combine,
  * enqueued on `stream` with no host synchronisation.
  *   x, w_router, bias          as moe_route
@@ -222,7 +298,8 @@ int moe_combine(const moe_shape* s, const void* y_perm, const int32_t* slot_pos,
  * INT4 experts: the activations are scaled per row by a power of two and rounded to f16 (exact for bf16
  * inputs from 2^-28 of the row's largest |x| up); the weights enter the MMAs as exact f16 integer codes
  * with a per-group offset that is removed in fp32, and the bf16 group scales multiply the fp32 group sums.
- *   side_stream  NULL, or a second stream of the caller's: with bf16 experts and a shared expert, the shared
+ * INT8 experts: x is quantised per token (moe_quantize_int8) and the experts run as moe_expert_ffn_int8.
+ *   side_stream  NULL, or a second stream of the caller's: with bf16 or INT8 experts and a shared expert, the shared
  *                expert (which needs only x) runs there, forked from `stream` by an event at the start and
  *                joined back before the combine, so that it overlaps the routing, grouping and routed experts.
  *                The output is the same bit for bit.  All work is complete once `stream` passes the call's end.
@@ -250,7 +327,7 @@ int moe_backward_workspace_size(const moe_shape* s, size_t* bytes);
  * The routing decision (top-k, capacity drops) passes no gradient; the gate values, their renormalisation,
  * the softmax and the load-balance statistic aux = E sum_e f_e P_e (f_e counts, constant) do.  The forward's
  * routing, grouping and [g | u] are recomputed here; h and y are not (the gate gradient <dout, y> is taken as
- * <act(g) u, dout W2>).  bf16 experts only (MOE_UNSUPPORTED_SHAPE for INT4).
+ * <act(g) u, dout W2>).  bf16 experts only (MOE_UNSUPPORTED_SHAPE for INT4 and INT8).
  *   x, w_router, bias, w13, w13_sh   as moe_forward (w13_sh NULL when H_s == 0)
  *   w13t, w2t, w13t_sh, w2t_sh       transposes of w13, w2, w13_sh, w2_sh (moe_transpose_experts); the down
  *                                    projections enter only through these

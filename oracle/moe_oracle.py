@@ -45,6 +45,11 @@ What it computes, and where each step is defined on the pages it follows:
    The float decisions (max, division, rounding to bf16, rint) are taken in
    fp32, the precision the library's quantiser uses.
 
+8. Gradients of steps 4 and 6 on their own: dx_t = sum_j dx_perm[slot(t,j)], and for the combine
+   dy_perm[slot(t,j)] = w_tj dout_t, dw_tj = <dout_t, y_perm[slot(t,j)]>.
+9. Symmetric 8-bit rows: s = max|x| / 127 (fp32), q = rint(127 x / max|x|), s = 0 and q = 0 below 2^-119; and the
+   gated expert on such codes, h rounded to bf16 and quantised the same way between its two products.
+
 Parity pins: every function here is checked by ``tests/test_oracle_*.py``
 against closed forms, textbook values (``tests/golden``), brute force on tiny
 inputs, the dense compute-all-experts-then-mask evaluation (kieve-moe "Tests":
@@ -509,3 +514,57 @@ def dequantize_int4_g128(packed, scales) -> np.ndarray:
     *lead, N, K = q.shape
     s = np.asarray(scales, np.float64)
     return (q.reshape(*lead, N, K // GROUP, GROUP) * s[..., None]).reshape(*lead, N, K)
+
+
+# ---------------------------------------------------------------- step 8: gradients of the grouping and the combine
+
+def permute_backward(dx_perm, slot_pos, add=None) -> np.ndarray:
+    """dx [T, d] = sum over the kept slots of dx_perm rows, plus ``add``; slots of -1 contribute nothing."""
+    dx_perm = np.asarray(dx_perm, np.float64)
+    T, k = slot_pos.shape
+    dx = np.zeros((T, dx_perm.shape[1])) if add is None else np.array(add, np.float64)
+    for t in range(T):
+        for j in range(k):
+            if slot_pos[t, j] >= 0:
+                dx[t] += dx_perm[slot_pos[t, j]]
+    return dx
+
+
+def combine_backward(dout, y_perm, slot_pos, w):
+    """(dy_perm [R, d], dw [T, k]) of out_t = sum_j w_tj y_perm[slot(t, j)]; rows no slot fills get zero."""
+    dout, y_perm = np.asarray(dout, np.float64), np.asarray(y_perm, np.float64)
+    T, k = slot_pos.shape
+    dy, dw = np.zeros(y_perm.shape), np.zeros((T, k))
+    for t in range(T):
+        for j in range(k):
+            r = slot_pos[t, j]
+            if r >= 0:
+                dy[r] = float(w[t, j]) * dout[t]
+                dw[t, j] = float(dout[t] @ y_perm[r])
+    return dy, dw
+
+
+# ---------------------------------------------------------------- step 9: 8-bit integer experts
+
+def quantize_rows_int8(x):
+    """(codes as float64 integers [rows, K], scales float32 [rows]) of finite rows."""
+    x = np.asarray(x, np.float64)
+    m = np.abs(x).max(axis=1)
+    fine = m >= 2.0 ** -119
+    q = np.rint(127.0 * x / np.where(fine, m, 1.0)[:, None])     # 127 x is exact for bf16 and fp32 values
+    q[~fine] = 0.0
+    s = np.where(fine, m.astype(np.float32) / np.float32(127.0), np.float32(0.0)).astype(np.float32)
+    return q, s
+
+
+def expert_ffn_int8(xq, xs, w13q, s13, w2q, s2, act: int):
+    """y of one expert on codes xq [n, d] with scales xs [n] (float64, not rounded), and h (bf16 values), the codes
+    of h and their scales."""
+    H = w2q.shape[1]
+    z = (np.asarray(xq, np.float64) @ np.asarray(w13q, np.float64).T) * np.asarray(xs, np.float64)[:, None] \
+        * np.asarray(s13, np.float64)[None]
+    g, u = z[:, :H], z[:, H:]
+    h = bf16_round((silu(g) if act == ACT_SWIGLU else gelu_erf(g)) * u).astype(np.float64)
+    hq, hs = quantize_rows_int8(h)
+    y = (hq @ np.asarray(w2q, np.float64).T) * hs.astype(np.float64)[:, None] * np.asarray(s2, np.float64)[None]
+    return y, h, hq, hs

@@ -7,12 +7,15 @@ library is missing or no CUDA device is present, calls raise.
 
 The entry points mirror the C ABI in ``include/moe_b200.h``:
 ``moe_route``, ``moe_route_from_logits``, ``moe_permute``, ``moe_expert_ffn``,
-``moe_combine``, ``moe_forward``, ``moe_quantize_int4``, plus
-``moe_workspace_size``, ``moe_capacity``, ``moe_get_status``.
+``moe_combine``, ``moe_forward``, ``moe_quantize_int4``, the 8-bit integer experts (``moe_quantize_int8``,
+``moe_permute_int8``, ``moe_expert_ffn_int8``), the gradients of the grouping and of the combine
+(``moe_permute_backward``, ``moe_combine_backward``), plus ``moe_workspace_size``, ``moe_capacity``,
+``moe_get_status``.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -22,7 +25,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_b200.so")
 
 ACT_SWIGLU, ACT_GEGLU = 0, 1
-WFMT_BF16, WFMT_INT4_G128 = 0, 1
+WFMT_BF16, WFMT_INT4_G128, WFMT_INT8 = 0, 1, 2
+DTYPE_CODE = {torch.bfloat16: 0, torch.float32: 1}
 FLAG_SINGLE_CTA_GEMM = 1
 STATUS = {0: "MOE_OK", 1: "MOE_INVALID_ARGUMENT", 2: "MOE_UNSUPPORTED_SHAPE", 3: "MOE_WORKSPACE_TOO_SMALL",
           4: "MOE_CUDA_ERROR", 5: "MOE_DEVICE_TIMEOUT"}
@@ -31,7 +35,9 @@ EXPORTED = ["moe_grouped_rows", "moe_capacity", "moe_workspace_size", "moe_route
             "moe_permute", "moe_expert_ffn", "moe_combine", "moe_forward", "moe_quantize_int4", "moe_get_status",
             "moe_set_wait_limit_ns", "moe_selftest_wait_timeout", "moe_launch_count", "moe_status_string",
             "moe_permute_noalloc", "moe_transpose_experts", "moe_backward_workspace_size", "moe_backward_x",
-            "moe_backward", "moe_route_tree_workspace_size", "moe_route_tree"]
+            "moe_backward", "moe_route_tree_workspace_size", "moe_route_tree", "moe_quantize_int8",
+            "moe_permute_int8", "moe_expert_ffn_int8_workspace_size", "moe_expert_ffn_int8", "moe_combine_backward",
+            "moe_permute_backward"]
 
 
 class MoeError(RuntimeError):
@@ -94,6 +100,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_backward": (ctypes.c_int, [S] + [_P] * 10 + [ctypes.c_float] + [_P] * 7 + [sz, _P, _P]),
         "moe_route_tree_workspace_size": (ctypes.c_int, [S, i32, i32, ctypes.POINTER(sz)]),
         "moe_route_tree": (ctypes.c_int, [S, i32, i32] + [_P] * 8 + [sz, _P]),
+        "moe_quantize_int8": (ctypes.c_int, [_P, i32, i64, i32, _P, _P, _P]),
+        "moe_permute_int8": (ctypes.c_int, [S] + [_P] * 11 + [sz, _P]),
+        "moe_expert_ffn_int8_workspace_size": (ctypes.c_int, [S, i32, i64, ctypes.POINTER(sz)]),
+        "moe_expert_ffn_int8": (ctypes.c_int, [S, i32, i32, i64] + [_P] * 10 + [sz, _P]),
+        "moe_combine_backward": (ctypes.c_int, [S] + [_P] * 8),
+        "moe_permute_backward": (ctypes.c_int, [S, _P, i32, _P, _P, _P, i32, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -119,19 +131,53 @@ def _ptr(t):
         raise ValueError("device tensor expected")
     if not t.is_contiguous():
         raise ValueError("contiguous tensor expected")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+# The current stream's handle without a Stream object around it (0.1 us a call instead of 3.2), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _want(t, dtype, shape, name):
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+_HERE_CTX = contextlib.nullcontext()
+
+
+def _on(stream, *tensors):
+    """Context of a call on these tensors: their one device current, and `stream` (or that device's current stream)
+    the one that outputs and scratch are allocated for."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+            if dev.type != "cuda":
+                raise ValueError("device tensor expected")
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if stream is None and dev.index == torch.cuda.current_device():
+        return _HERE_CTX
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream of {stream.device}, tensors on {dev}")
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(dev))
+    if stream is not None:
+        ctx.enter_context(torch.cuda.stream(stream))
+    return ctx
 
 
 _ws_cache: dict = {}
@@ -262,8 +308,16 @@ def moe_permute_noalloc(shape: MoeShape, x, topk_idx, *, stream=None):
 def moe_expert_ffn(shape: MoeShape, x_grouped, w13, w2, *, hidden=None, group_start=None, group_rows=None,
                    s13=None, s2=None, h=None, y=None, want_h=True, stream=None):
     """Grouped gated expert FFN.  Returns (h, y); with ``want_h=False`` (bf16 experts of hidden 128 or 256) h
-    stays on chip in the fused kernel and None is returned in its place."""
+    stays on chip in the fused kernel and None is returned in its place.  INT8 experts: the rows are quantised
+    (moe_quantize_int8) and go through moe_expert_ffn_int8; h is None."""
     hidden = shape.H if hidden is None else hidden
+    if shape.wfmt == WFMT_INT8:
+        if h is not None:
+            raise ValueError("moe_expert_ffn: INT8 experts return no h")
+        _want(x_grouped, torch.bfloat16, (x_grouped.shape[0], shape.d), "x_grouped")
+        xq, xs = moe_quantize_int8(x_grouped, stream=stream)
+        return None, moe_expert_ffn_int8(shape, xq, xs, w13, s13, w2, s2, hidden=hidden, group_start=group_start,
+                                         group_rows=group_rows, y=y, stream=stream)
     R = x_grouped.shape[0]
     n_groups = w13.shape[0]
     dev = x_grouped.device
@@ -417,6 +471,124 @@ def moe_quantize_int4(w, *, q=None, scales=None, stream=None):
     rc = _L().moe_quantize_int4(_ptr(w), rows, K, _ptr(q), _ptr(scales), _stream(stream))
     _check(rc, "moe_quantize_int4")
     return q, scales
+
+
+def moe_quantize_int8(x, *, q=None, scales=None, stream=None):
+    """x [..., K] bf16 or fp32 -> (q [..., K] int8, scales [...] fp32): one scale per row, x ~ q * scale."""
+    if x.dtype not in DTYPE_CODE:
+        raise TypeError(f"x: expected torch.bfloat16 or torch.float32, got {x.dtype}")
+    if x.dim() < 1:
+        raise ValueError("x: expected at least one dimension")
+    K = x.shape[-1]
+    rows = x.numel() // K if K else 0
+    with _on(stream, x, q, scales):
+        if q is None:
+            q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        if scales is None:
+            scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        _want(q, torch.int8, x.shape, "q")
+        _want(scales, torch.float32, x.shape[:-1], "scales")
+        _check(_L().moe_quantize_int8(_ptr(x), DTYPE_CODE[x.dtype], rows, K, _ptr(q), _ptr(scales), _stream()),
+               "moe_quantize_int8")
+    return q, scales
+
+
+def moe_permute_int8(shape: MoeShape, x, topk_idx, *, ws=None, stream=None):
+    """moe_permute with the rows quantised on the way: a dict with xq_perm [R, d] int8 and xs_perm [R] fp32 in the
+    place of x_perm.  With a capacity, the rows behind an expert's kept ones hold nothing in particular, and row_src
+    is -1 there."""
+    T, d, E, k = shape.T, shape.d, shape.E, shape.k
+    _want(x, torch.bfloat16, (T, d), "x")
+    _want(topk_idx, torch.int32, (T, k), "topk_idx")
+    dev, R = x.device, shape.R
+    with _on(stream, x, topk_idx, ws):
+        i32 = dict(dtype=torch.int32, device=dev)
+        out = dict(slot_pos=torch.empty(T, k, **i32), drop_mask=torch.empty(T, k, dtype=torch.uint8, device=dev),
+                   counts=torch.empty(E, **i32), kept=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32),
+                   row_src=torch.full((R,), -1, **i32) if shape.capacity > 0 else torch.empty(R, **i32),
+                   xq_perm=torch.empty(R, d, dtype=torch.int8, device=dev),
+                   xs_perm=torch.empty(R, dtype=torch.float32, device=dev))
+        if ws is None:
+            ws = torch.empty(moe_workspace_size(shape), dtype=torch.uint8, device=dev)
+        rc = _L().moe_permute_int8(ctypes.byref(shape), _ptr(x), _ptr(topk_idx), _ptr(out["slot_pos"]),
+                                   _ptr(out["drop_mask"]), _ptr(out["counts"]), _ptr(out["kept"]),
+                                   _ptr(out["offsets"]), _ptr(out["row_src"]), _ptr(out["xq_perm"]),
+                                   _ptr(out["xs_perm"]), _ptr(ws), ws.numel(), _stream())
+        _check(rc, "moe_permute_int8")
+    return out
+
+
+def moe_expert_ffn_int8(shape: MoeShape, xq, xs, w13, s13, w2, s2, *, hidden=None, group_start=None,
+                        group_rows=None, y=None, ws=None, stream=None):
+    """Grouped gated expert FFN in 8-bit integers (shape.wfmt == WFMT_INT8): xq [R, d] int8 with one scale a row
+    xs [R], w13 [n, 2 hidden, d] and w2 [n, d, hidden] int8 with one scale an output channel.  Returns y [R, d]
+    bf16; rows outside every group are not written."""
+    hidden = shape.H if hidden is None else hidden
+    n, R, d = w13.shape[0], xq.shape[0], shape.d
+    _want(xq, torch.int8, (R, d), "xq")
+    _want(xs, torch.float32, (R,), "xs")
+    _want(w13, torch.int8, (n, 2 * hidden, d), "w13")
+    _want(w2, torch.int8, (n, d, hidden), "w2")
+    _want(s13, torch.float32, (n, 2 * hidden), "s13")
+    _want(s2, torch.float32, (n, d), "s2")
+    for t, name in ((group_start, "group_start"), (group_rows, "group_rows")):
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < n):
+            raise ValueError(f"{name}: expected at least {n} int32 values")
+    with _on(stream, xq, xs, w13, s13, w2, s2, group_start, group_rows, y, ws):
+        if y is None:
+            y = torch.empty(R, d, dtype=torch.bfloat16, device=xq.device)
+        _want(y, torch.bfloat16, (R, d), "y")
+        if ws is None:
+            nb = ctypes.c_size_t(0)
+            _check(_L().moe_expert_ffn_int8_workspace_size(ctypes.byref(shape), hidden, R, ctypes.byref(nb)),
+                   "moe_expert_ffn_int8_workspace_size")
+            ws = torch.empty(int(nb.value), dtype=torch.uint8, device=xq.device)
+        rc = _L().moe_expert_ffn_int8(ctypes.byref(shape), n, hidden, R, _ptr(xq), _ptr(xs), _ptr(group_start),
+                                      _ptr(group_rows), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(y), _ptr(ws),
+                                      ws.numel(), _stream())
+        _check(rc, "moe_expert_ffn_int8")
+    return y
+
+
+def moe_combine_backward(shape: MoeShape, dout, y_perm, slot_pos, topk_w, *, kept=None, want_dw=True, stream=None):
+    """Gradient of moe_combine: dict(dy_perm [R, d] bf16, dtopk_w [T, k] fp32 or None); that of y_shared is dout.
+    With a capacity and ``kept`` (of moe_permute), rows that no token fills come back zero; without ``kept`` they
+    hold nothing in particular."""
+    T, d, k, R = shape.T, shape.d, shape.k, shape.R
+    _want(dout, torch.bfloat16, (T, d), "dout")
+    _want(y_perm, torch.bfloat16, (R, d), "y_perm")
+    _want(slot_pos, torch.int32, (T, k), "slot_pos")
+    _want(topk_w, torch.float32, (T, k), "topk_w")
+    if kept is not None:
+        _want(kept, torch.int32, (shape.E,), "kept")
+    with _on(stream, dout, y_perm, slot_pos, topk_w, kept):
+        dy = torch.empty(R, d, dtype=torch.bfloat16, device=dout.device)
+        dw = torch.empty(T, k, dtype=torch.float32, device=dout.device) if want_dw else None
+        rc = _L().moe_combine_backward(ctypes.byref(shape), _ptr(dout), _ptr(y_perm), _ptr(slot_pos), _ptr(topk_w),
+                                       _ptr(kept) if shape.capacity > 0 else None, _ptr(dy), _ptr(dw), _stream())
+        _check(rc, "moe_combine_backward")
+    return dict(dy_perm=dy, dtopk_w=dw)
+
+
+def moe_permute_backward(shape: MoeShape, dx_perm, slot_pos, *, add=None, dtype=torch.float32, out=None,
+                         stream=None):
+    """Gradient of moe_permute's row moves: dx [T, d] (dtype bf16 or fp32) = the sum of each token's kept rows of
+    dx_perm [R, d] (bf16 or fp32), plus ``add`` [T, d] of that dtype when given.  ``out`` may be ``add``."""
+    T, d, R = shape.T, shape.d, shape.R
+    if dx_perm.dtype not in DTYPE_CODE or dtype not in DTYPE_CODE:
+        raise TypeError(f"dx_perm, dtype: expected torch.bfloat16 or torch.float32, got {dx_perm.dtype}, {dtype}")
+    _want(dx_perm, dx_perm.dtype, (R, d), "dx_perm")
+    _want(slot_pos, torch.int32, (T, shape.k), "slot_pos")
+    if add is not None:
+        _want(add, dtype, (T, d), "add")
+    with _on(stream, dx_perm, slot_pos, add, out):
+        if out is None:
+            out = torch.empty(T, d, dtype=dtype, device=dx_perm.device)
+        _want(out, dtype, (T, d), "out")
+        rc = _L().moe_permute_backward(ctypes.byref(shape), _ptr(dx_perm), DTYPE_CODE[dx_perm.dtype],
+                                       _ptr(slot_pos), _ptr(add), _ptr(out), DTYPE_CODE[dtype], _stream())
+        _check(rc, "moe_permute_backward")
+    return out
 
 
 def moe_get_status(stream=None):

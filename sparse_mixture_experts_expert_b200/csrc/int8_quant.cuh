@@ -1,0 +1,169 @@
+// Symmetric 8-bit quantisation of rows: one fp32 scale a row (a token of the activations, an output channel of the
+// weights), the form the 8-bit integer expert products take (int8_gemm.cuh).  With m = max|x_r| of row r:
+//   s_r = m / 127 (IEEE),   q = rint(127 x / m), ties to even, in [-127, 127],   x ~ q s_r.
+// A row with m < 2^-119 (zeros among them) gets s = 0, q = 0, so that 127 / m stays finite.  A row that holds an
+// infinity or a NaN gets that as its scale, so what is computed from it is not finite either.
+//
+// q is computed as fma(x, r, 1.5 2^23) with r = 127 / m rounded up: the sum's low byte is rint(x r).  For bf16 rows
+// this is exactly rint(127 x / m): with 8-bit significands a quotient that is no tie lies at least 1/510 away from
+// every tie, far more than the 2^-17 that r's rounding moves it; of the ties, those with 127 / m a power of two are
+// exact, and the others all have |x| = m / 2, where the quotient 63.5 rounds to 64 and r >= 127 / m keeps it there.
+// (For fp32 rows a quotient within 2^-16 of a tie may go either way.)
+// The pass is bound by HBM: the row stays in registers between the maximum and the codes.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr float kQuantTiny = 1.5046327690525280e-36f;   // 2^-119
+constexpr int kQuantVec = 4;                             // 8-element vectors a thread keeps between the two passes
+
+// Eight elements as they lie in memory.
+template <typename T> struct RawVec;
+template <> struct RawVec<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  // maximum of |x| as bits: a NaN's exceed infinity's, infinity's every number's
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu),
+                                __vmaxu2(a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
+    return max(m << 16, m & 0xFFFF0000u);
+  }
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? a.x : i < 4 ? a.y : i < 6 ? a.z : a.w;
+    return (i & 1) ? bf16hi(w) : bf16lo(w);
+  }
+};
+template <> struct RawVec<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ static uint32_t mag(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+  __device__ __forceinline__ uint32_t top() const {
+    return max(max(max(mag(a.x), mag(a.y)), max(mag(a.z), mag(a.w))),
+               max(max(mag(b.x), mag(b.y)), max(mag(b.z), mag(b.w))));
+  }
+  __device__ __forceinline__ float at(int i) const {
+    return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
+  }
+};
+
+// Scale and multiplier of a row with maximum m.
+__device__ __forceinline__ void quant_scale(float m, float& s, float& r) {
+  if (m < kQuantTiny) {
+    s = 0.f;
+    r = 0.f;
+  } else {
+    s = __fdiv_rn(m, 127.0f);
+    r = __fdiv_ru(127.0f, m);
+  }
+}
+
+// rint(x r) in the low byte (|x r| <= 127 (1 + 2^-23)).
+__device__ __forceinline__ uint32_t quant_code(float x, float r) { return __float_as_uint(fmaf(x, r, 12582912.0f)); }
+__device__ __forceinline__ uint32_t pack_codes(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3) {
+  return __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
+}
+
+template <typename T>
+__device__ __forceinline__ uint2 quant_vec(const RawVec<T>& v, float r) {
+  return make_uint2(pack_codes(quant_code(v.at(0), r), quant_code(v.at(1), r), quant_code(v.at(2), r),
+                               quant_code(v.at(3), r)),
+                    pack_codes(quant_code(v.at(4), r), quant_code(v.at(5), r), quant_code(v.at(6), r),
+                               quant_code(v.at(7), r)));
+}
+
+// One row by TPR threads (a warp, or the CTA's 256): maximum, then codes handed to put(vector index, 8 codes) and
+// the scale returned.  Rows longer than TPR * kQuantVec vectors are read a second time past that.
+template <int TPR, typename T, typename Put>
+__device__ __forceinline__ float quant_row(const T* __restrict__ x, int K, uint32_t* s_max, Put put) {
+  const int nvec = K >> 3;
+  const int th = TPR == 32 ? lane_id() : (int)threadIdx.x;
+  RawVec<T> v[kQuantVec];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kQuantVec; ++i) {
+    const int c = th + i * TPR;
+    if (c < nvec) {
+      v[i].load(x + 8 * c);
+      m = max(m, v[i].top());
+    }
+  }
+  for (int c = th + kQuantVec * TPR; c < nvec; c += TPR) {
+    RawVec<T> u;
+    u.load(x + 8 * c);
+    m = max(m, u.top());
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (TPR > 32) {
+    if (lane_id() == 0) s_max[warp_id()] = m;
+    __syncthreads();
+    m = s_max[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 32; ++i) m = max(m, s_max[i]);
+    __syncthreads();   // s_max may be rewritten for the next row
+  }
+  float s, r;
+  quant_scale(__uint_as_float(m), s, r);
+#pragma unroll
+  for (int i = 0; i < kQuantVec; ++i) {
+    const int c = th + i * TPR;
+    if (c < nvec) put(c, quant_vec(v[i], r));
+  }
+  for (int c = th + kQuantVec * TPR; c < nvec; c += TPR) {
+    RawVec<T> u;
+    u.load(x + 8 * c);
+    put(c, quant_vec(u, r));
+  }
+  return s;
+}
+
+// Rows 0 .. rows-1 of x [rows, K]; one row per warp (TPR 32) or per CTA (TPR 256).
+template <int TPR, typename T>
+__global__ void __launch_bounds__(256) k_quant_rows(const T* __restrict__ x, long long rows, int K,
+                                                    int8_t* __restrict__ q, float* __restrict__ scale) {
+  pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
+  __shared__ uint32_t s_max[8];
+  const long long r = TPR == 32 ? (long long)blockIdx.x * 8 + warp_id() : (long long)blockIdx.x;
+  if (r >= rows) return;
+  const float s = quant_row<TPR>(x + r * K, K, s_max, [&](int c, uint2 v) {
+    reinterpret_cast<uint2*>(q + r * K)[c] = v;
+  });
+  if ((TPR == 32 ? lane_id() : (int)threadIdx.x) == 0) scale[r] = s;
+}
+
+// The dispatch: token t's row is read once, quantised, and its codes and scale written to the grouped row of each of
+// its kept slots; with q_tok, also to row t there (the shared expert's input).
+template <int TPR, int KMAX>
+__global__ void __launch_bounds__(256) k_quant_slots(const __nv_bfloat16* __restrict__ x,
+                                                     const int32_t* __restrict__ slot_pos, int T, int d, int k, int R,
+                                                     int8_t* __restrict__ q, float* __restrict__ scale,
+                                                     int8_t* __restrict__ q_tok, float* __restrict__ s_tok) {
+  pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
+  __shared__ uint32_t s_max[8];
+  const long long t = TPR == 32 ? (long long)blockIdx.x * 8 + warp_id() : (long long)blockIdx.x;
+  if (t >= T) return;
+  int p[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+    p[j] = j < k ? slot_pos[t * k + j] : -1;
+    if ((unsigned)p[j] >= (unsigned)R) p[j] = -1;
+  }
+  const float s = quant_row<TPR>(x + t * d, d, s_max, [&](int c, uint2 v) {
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+      if (p[j] >= 0) reinterpret_cast<uint2*>(q + (size_t)p[j] * d)[c] = v;
+    if (q_tok != nullptr) reinterpret_cast<uint2*>(q_tok + t * d)[c] = v;
+  });
+  if ((TPR == 32 ? lane_id() : (int)threadIdx.x) == 0) {
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+      if (p[j] >= 0) scale[p[j]] = s;
+    if (q_tok != nullptr) s_tok[t] = s;
+  }
+}
+
+}  // namespace moe

@@ -13,9 +13,12 @@
 #include "expert_fused.cuh"
 #include "gemm_tc.cuh"
 #include "int4_gemm.cuh"
+#include "int8_gemm.cuh"
+#include "int8_quant.cuh"
 #include "permute.cuh"
 #include "quant.cuh"
 #include "router.cuh"
+#include "sort_grad.cuh"
 #include "tree_router.cuh"
 #include "wgrad.cuh"
 
@@ -92,7 +95,8 @@ static int check_shape(const moe_shape* s) {
   if (s->H_s < 0 || s->H_s % 16 != 0 || s->H_s > 65536) return MOE_UNSUPPORTED_SHAPE;
   if (s->capacity < 0) return MOE_INVALID_ARGUMENT;
   if (s->act != MOE_ACT_SWIGLU && s->act != MOE_ACT_GEGLU) return MOE_INVALID_ARGUMENT;
-  if (s->wfmt != MOE_WFMT_BF16 && s->wfmt != MOE_WFMT_INT4_G128) return MOE_INVALID_ARGUMENT;
+  if (s->wfmt != MOE_WFMT_BF16 && s->wfmt != MOE_WFMT_INT4_G128 && s->wfmt != MOE_WFMT_INT8)
+    return MOE_INVALID_ARGUMENT;
   if (s->renorm != 0 && s->renorm != 1) return MOE_INVALID_ARGUMENT;
   if (s->flags & ~MOE_FLAG_SINGLE_CTA_GEMM) return MOE_INVALID_ARGUMENT;
   if (s->wfmt == MOE_WFMT_INT4_G128 && (s->d % 128 != 0 || s->H % 128 != 0 || s->H_s % 128 != 0))
@@ -139,8 +143,15 @@ static int router_splits(const moe_shape* s, int* k_per_split) {
 
 // ------------------------------------------------------------------ workspace layout
 
+// Regions of the 8-bit integer experts: xq / xs the input rows' codes and scales, h in bf16, hq / hs its codes and
+// scales.  Offsets from the workspace's start.
+struct I8Work {
+  size_t xq, xs, h, hq, hs;
+};
+
 struct Workspace {
   size_t part, wsplit, wnorm, xcs, xrs, xq, i4part, cnt, psum, idx, w, counts, fP, slot, drop, kept, offs, xperm, h, yperm, hs, ys, shtab;
+  I8Work i8r, i8s;   // INT8: codes and scales of the routed rows and of the tokens (shared expert)
   size_t cidx, ncand, zmax, snc, zex, ecount, elist, xnorm2;   // certified selection over the screening logits
   size_t total;
 };
@@ -182,10 +193,22 @@ static Workspace ws_layout(const moe_shape* s) {
   L.drop = take((size_t)s->T * s->k);
   L.kept = take((size_t)s->E * 4);
   L.offs = take((size_t)(s->E + 1) * 4);
-  L.xperm = take((size_t)R * s->d * 2);
-  L.h = take((size_t)R * s->H * 2);
+  const bool i8 = s->wfmt == MOE_WFMT_INT8;
+  auto take_i8 = [&](I8Work& W, size_t rows, int hidden) {
+    W.xq = take(rows * s->d);
+    W.xs = take(rows * 4);
+    W.h = take(rows * hidden * 2);
+    W.hq = take(rows * hidden);
+    W.hs = take(rows * 4);
+  };
+  if (i8) {
+    take_i8(L.i8r, (size_t)R, s->H);
+    if (s->H_s > 0) take_i8(L.i8s, (size_t)s->T, s->H_s);
+  }
+  L.xperm = take(i8 ? 16 : (size_t)R * s->d * 2);
+  L.h = take(i8 ? 16 : (size_t)R * s->H * 2);
   L.yperm = take((size_t)R * s->d * 2);
-  L.hs = take((size_t)s->T * std::max(s->H_s, 16) * 2);
+  L.hs = take(i8 ? 16 : (size_t)s->T * std::max(s->H_s, 16) * 2);
   L.ys = take((size_t)s->T * s->d * 2);
   L.shtab = take(64);
   L.cidx = take((size_t)s->T * kSelMaxCand);
@@ -658,6 +681,155 @@ static int int4_gemm(bool glu, int act, const void* A, long long R, int K, const
     }
     return MOE_OK;
   }
+}
+
+// ------------------------------------------------------------------ 8-bit integer experts
+
+// Byte tensor [outer..., rows, K] (K innermost), box = 128 x box_rows (x 1).
+static int make_map_i8(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, int box_rows) {
+  EncodeTiledFn enc = get_encoder();
+  if (!enc) return MOE_CUDA_ERROR;
+  cuuint64_t strides[2] = {dims[0], rank == 3 ? dims[0] * dims[1] : 0};
+  cuuint32_t box[3] = {(cuuint32_t)kI8BK, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : MOE_CUDA_ERROR;
+}
+
+template <int MODE, int BN, int CG>
+static int launch_i8_t(const CUtensorMap& ta, const CUtensorMap& tb, const I8Params& p, long long ub_mtiles,
+                       cudaStream_t st) {
+  using Cfg = I8Cfg<BN, CG>;
+  constexpr int OUTN = (MODE == kModeSwiGLU || MODE == kModeGeGLU) ? BN / 2 : BN;
+  static std::atomic<unsigned long long> done_mask{0};
+  const unsigned long long bit = 1ull << (current_device() & 63);
+  if (!(done_mask.load(std::memory_order_relaxed) & bit)) {
+    MOE_CUDA_TRY(cudaFuncSetAttribute(k_int8_gemm<MODE, BN, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)Cfg::kSmemBytes));
+    done_mask.fetch_or(bit);
+  }
+  const long long tiles = ub_mtiles * cdiv(p.N, OUTN);
+  const int units = (int)std::max<long long>(1, std::min<long long>(num_sms() / CG, tiles));
+  MOE_CUDA_TRY(launch_pdl(k_int8_gemm<MODE, BN, CG>, dim3((unsigned)(CG * units)), dim3(kI8Threads), Cfg::kSmemBytes,
+                          st, (unsigned)CG, ta, tb, p));
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+// out[R, N] bf16 = epilogue(codes A[R, K] . codes B_g^T) with row scales a_scale and channel scales b_scale.
+static int int8_gemm(int mode, const void* A, const float* a_scale, long long R, int K, const void* B,
+                     const float* b_scale, int n_groups, int b_rows, int up_row0, int N, const int32_t* gstart,
+                     const int32_t* grows, void* out, cudaStream_t st, bool allow_pair) {
+  const bool glu = mode != kModePlain;
+  const long long ub_m = grows ? (R / kBM + n_groups) : cdiv(R, kBM);
+  const int BN = pick_bn(glu, N, ub_m);
+  const bool pair = use_pair_gemm(mode, BN, R, n_groups, allow_pair);
+  CUtensorMap ta, tb;
+  const cuuint64_t da[2] = {(cuuint64_t)K, (cuuint64_t)R};
+  const cuuint64_t db[3] = {(cuuint64_t)K, (cuuint64_t)b_rows, (cuuint64_t)n_groups};
+  int rc = make_map_i8(&ta, A, 2, da, kI8ABox);
+  if (rc) return rc;
+  rc = make_map_i8(&tb, B, 3, db, (glu || pair) ? BN / 2 : BN);
+  if (rc) return rc;
+  I8Params p;
+  p.group_start = gstart;
+  p.group_rows = grows;
+  p.n_groups = n_groups;
+  p.R = R;
+  p.K = K;
+  p.N = N;
+  p.up_row0 = up_row0;
+  p.b_rows = b_rows;
+  p.a_scale = a_scale;
+  p.b_scale = b_scale;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  const long long TM = (long long)kBM * (pair ? 2 : 1);
+  const long long ub = grows ? (R / TM + n_groups) : cdiv(R, TM);
+  if (pair) {
+    if (mode == kModePlain) return launch_i8_t<kModePlain, 256, 2>(ta, tb, p, ub, st);
+    if (mode == kModeSwiGLU) return launch_i8_t<kModeSwiGLU, 256, 2>(ta, tb, p, ub, st);
+    return launch_i8_t<kModeGeGLU, 256, 2>(ta, tb, p, ub, st);
+  }
+#define MOE_I8_CASE(M_, BN_) \
+  if (mode == M_ && BN == BN_) return launch_i8_t<M_, BN_, 1>(ta, tb, p, ub, st);
+  MOE_I8_CASE(kModePlain, 256) MOE_I8_CASE(kModePlain, 128) MOE_I8_CASE(kModePlain, 64)
+  MOE_I8_CASE(kModeSwiGLU, 256) MOE_I8_CASE(kModeSwiGLU, 128) MOE_I8_CASE(kModeSwiGLU, 64)
+  MOE_I8_CASE(kModeGeGLU, 256) MOE_I8_CASE(kModeGeGLU, 128) MOE_I8_CASE(kModeGeGLU, 64)
+#undef MOE_I8_CASE
+  return MOE_UNSUPPORTED_SHAPE;
+}
+
+// Codes and scales of x [rows, K]: a row per warp up to 1024 columns (four 8-element vectors a lane stay in
+// registers), else a row per CTA.
+template <typename T>
+static int launch_quant_rows(const T* x, long long rows, int K, int8_t* q, float* scale, cudaStream_t st) {
+  if (K <= 32 * 8 * kQuantVec)
+    MOE_LAUNCH((k_quant_rows<32, T>), (unsigned)cdiv(rows, 8), 256, 0, st, x, rows, K, q, scale);
+  else
+    MOE_LAUNCH((k_quant_rows<256, T>), (unsigned)rows, 256, 0, st, x, rows, K, q, scale);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+// The tokens' codes and scales to the rows of their kept slots (and, with q_tok, to row t there).
+static int launch_quant_slots(const moe_shape* s, const void* x, const int32_t* slot, int8_t* q, float* scale,
+                              int8_t* q_tok, float* s_tok, cudaStream_t st) {
+  const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(x);
+  const int R = (int)grouped_rows(s);
+  const bool warp_rows = s->d <= 32 * 8 * kQuantVec;
+  const unsigned blocks = (unsigned)(warp_rows ? cdiv(s->T, 8) : s->T);
+#define MOE_QSLOT(N_)                                                                                             \
+  if (s->k <= N_) {                                                                                               \
+    if (warp_rows)                                                                                                \
+      MOE_LAUNCH((k_quant_slots<32, N_>), blocks, 256, 0, st, xb, slot, (int)s->T, s->d, s->k, R, q, scale, q_tok, \
+                 s_tok);                                                                                          \
+    else                                                                                                          \
+      MOE_LAUNCH((k_quant_slots<256, N_>), blocks, 256, 0, st, xb, slot, (int)s->T, s->d, s->k, R, q, scale,       \
+                 q_tok, s_tok);                                                                                   \
+    MOE_LAUNCH_CHECK();                                                                                           \
+    return MOE_OK;                                                                                                \
+  }
+  MOE_QSLOT(2) MOE_QSLOT(4) MOE_QSLOT(8) MOE_QSLOT(16)
+#undef MOE_QSLOT
+  return MOE_UNSUPPORTED_SHAPE;
+}
+
+// y = FFN of the codes xq (scales xs) over groups; h [R, hidden] bf16, hq [R, hidden] and hs [R] are scratch.
+static int int8_ffn(const moe_shape* s, int hidden, long long R, const void* xq, const float* xs,
+                    const int32_t* gstart, const int32_t* grows, int n_groups, const void* w13, const float* s13,
+                    const void* w2, const float* s2, void* h, void* hq, float* hs, void* y, cudaStream_t st) {
+  if (R == 0) return MOE_OK;
+  const bool pair = !(s->flags & MOE_FLAG_SINGLE_CTA_GEMM);
+  int rc = int8_gemm(s->act == MOE_ACT_SWIGLU ? kModeSwiGLU : kModeGeGLU, xq, xs, R, s->d, w13, s13, n_groups,
+                     2 * hidden, hidden, hidden, gstart, grows, h, st, pair);
+  if (rc) return rc;
+  const __nv_bfloat16* hb = reinterpret_cast<const __nv_bfloat16*>(h);
+  int8_t* hc = reinterpret_cast<int8_t*>(hq);
+  if (grows == nullptr) {
+    rc = launch_quant_rows(hb, R, hidden, hc, hs, st);
+    if (rc) return rc;
+  } else {
+    I8Params p{};
+    p.group_start = gstart;
+    p.group_rows = grows;
+    p.n_groups = n_groups;
+    p.R = R;
+    p.K = hidden;
+    const long long most = 8ll * num_sms();   // 256-thread CTAs resident at once
+    if (hidden <= 32 * 8 * kQuantVec)
+      MOE_LAUNCH((k_quant_groups<32>), (unsigned)std::min(most, cdiv(R, 8)), 256, 0, st, hb, p, hc, hs);
+    else
+      MOE_LAUNCH((k_quant_groups<256>), (unsigned)std::min(most, R), 256, 0, st, hb, p, hc, hs);
+    MOE_LAUNCH_CHECK();
+  }
+  return int8_gemm(kModePlain, hq, hs, R, hidden, w2, s2, n_groups, s->d, 0, s->d, gstart, grows, y, st, pair);
+}
+
+static size_t int8_ffn_bytes(int hidden, long long R) {
+  return align256((size_t)R * hidden * 2) + align256((size_t)R * hidden) + align256((size_t)R * 4);
 }
 
 // Gated expert FFN over groups of rows: h = act(A W1^T) * (A W3^T), y = h W2^T.
@@ -1224,6 +1396,7 @@ int moe_expert_ffn(const moe_shape* s, int32_t n_groups, int32_t hidden, int64_t
   if (hidden < 16 || hidden % 16 != 0) return MOE_UNSUPPORTED_SHAPE;
   if ((group_start == nullptr) != (group_rows == nullptr)) return MOE_INVALID_ARGUMENT;
   if (group_start == nullptr && n_groups != 1) return MOE_INVALID_ARGUMENT;
+  if (s->wfmt == MOE_WFMT_INT8) return MOE_INVALID_ARGUMENT;   // takes scratch: moe_expert_ffn_int8
   if (R == 0) return MOE_OK;
   if (!x_grouped || !w13 || !w2 || !y) return MOE_INVALID_ARGUMENT;
   if (h == nullptr && !fused_ffn_ok(s, hidden)) return MOE_INVALID_ARGUMENT;
@@ -1276,7 +1449,7 @@ int moe_forward(const moe_shape* s, const void* x, const float* w_router, const 
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(w13) || !aligned16(w2) || !aligned16(out) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return MOE_INVALID_ARGUMENT;
-  if (s->wfmt == MOE_WFMT_INT4_G128 &&
+  if (s->wfmt != MOE_WFMT_BF16 &&
       (!s13 || !s2 || !aligned16(s13) || !aligned16(s2) || (s->H_s > 0 && (!s13_sh || !s2_sh))))
     return MOE_INVALID_ARGUMENT;
   const Workspace L = ws_layout(s);
@@ -1294,8 +1467,16 @@ int moe_forward(const moe_shape* s, const void* x, const float* w_router, const 
   void* yperm = ws + L.yperm;
   const long long R = grouped_rows(s);
   const bool int4 = s->wfmt == MOE_WFMT_INT4_G128;
+  const bool i8 = s->wfmt == MOE_WFMT_INT8;
+  auto i8_codes = [&](const I8Work& W) { return reinterpret_cast<int8_t*>(ws + W.xq); };
+  auto i8_scales = [&](const I8Work& W) { return reinterpret_cast<float*>(ws + W.xs); };
+  auto i8_shared = [&](cudaStream_t st) {
+    return int8_ffn(s, s->H_s, s->T, i8_codes(L.i8s), i8_scales(L.i8s), nullptr, nullptr, 1, w13_sh,
+                    reinterpret_cast<const float*>(s13_sh), w2_sh, reinterpret_cast<const float*>(s2_sh),
+                    ws + L.i8s.h, ws + L.i8s.hq, reinterpret_cast<float*>(ws + L.i8s.hs), ws + L.ys, st);
+  };
 
-  // bf16 experts: the shared expert needs only x, so with a side stream it runs there from the start, beside the
+  // bf16 and INT8 experts: the shared expert needs only x, so with a side stream it runs there from the start, beside the
   // routing, grouping and routed experts, and joins before the combine.  (INT4: its activation copy is formed
   // with the routed one, so it stays in order.)
   void* ys = nullptr;
@@ -1305,8 +1486,15 @@ int moe_forward(const moe_shape* s, const void* x, const float* w_router, const 
     rc = fork.start(stream, side_stream);
     if (rc) return rc;
     ys = ws + L.ys;
-    rc = expert_ffn_impl(s, s->H_s, s->T, x, nullptr, nullptr, 1, w13_sh, s13_sh, w2_sh, s2_sh, ws + L.hs, ys,
-                         side_stream, Int4Scratch{nullptr, nullptr, nullptr});
+    if (i8) {
+      rc = launch_quant_rows(reinterpret_cast<const __nv_bfloat16*>(x), s->T, s->d, i8_codes(L.i8s),
+                             i8_scales(L.i8s), side_stream);
+      if (rc) return rc;
+      rc = i8_shared(side_stream);
+    } else {
+      rc = expert_ffn_impl(s, s->H_s, s->T, x, nullptr, nullptr, 1, w13_sh, s13_sh, w2_sh, s2_sh, ws + L.hs, ys,
+                           side_stream, Int4Scratch{nullptr, nullptr, nullptr});
+    }
     if (rc) return rc;
     rc = fork.end(side_stream);
     if (rc) return rc;
@@ -1316,10 +1504,28 @@ int moe_forward(const moe_shape* s, const void* x, const float* w_router, const 
   if (rc) return rc;
   const float* f_used = aux_f ? aux_f : reinterpret_cast<const float*>(ws + L.fP);
   const float* p_used = aux_p ? aux_p : reinterpret_cast<const float*>(ws + L.fP) + s->E;
-  // INT4: the grouped activation copy is formed by k_int4_act_prep from x and the slots, so no bf16 rows move
-  rc = launch_scatter(s, x, idx, cnt, cts, slot, drop_mask, nullptr, xperm, kept, offs, stream, !int4, f_used, p_used,
-                      aux);
+  // INT4 and INT8: the grouped activations are formed from x and the slots by k_int4_act_prep / k_quant_slots, so no
+  // bf16 rows move
+  rc = launch_scatter(s, x, idx, cnt, cts, slot, drop_mask, nullptr, xperm, kept, offs, stream, !int4 && !i8, f_used,
+                      p_used, aux);
   if (rc) return rc;
+  if (i8) {
+    const bool tok = s->H_s > 0 && !forked;   // the shared expert's input codes, written along
+    rc = launch_quant_slots(s, x, slot, i8_codes(L.i8r), i8_scales(L.i8r), tok ? i8_codes(L.i8s) : nullptr,
+                            tok ? i8_scales(L.i8s) : nullptr, stream);
+    if (rc) return rc;
+    rc = int8_ffn(s, s->H, R, i8_codes(L.i8r), i8_scales(L.i8r), offs, kept, s->E, w13,
+                  reinterpret_cast<const float*>(s13), w2, reinterpret_cast<const float*>(s2), ws + L.i8r.h,
+                  ws + L.i8r.hq, reinterpret_cast<float*>(ws + L.i8r.hs), yperm, stream);
+    if (rc) return rc;
+    if (tok) {
+      ys = ws + L.ys;
+      rc = i8_shared(stream);
+      if (rc) return rc;
+    }
+    if (forked && (rc = fork.wait(stream))) return rc;
+    return moe_combine(s, yperm, slot, w, ys, out, stream);
+  }
   const Int4Scratch scr = int4 ? Int4Scratch{reinterpret_cast<float*>(ws + L.xcs), reinterpret_cast<float*>(ws + L.xrs),
                                              ws + L.xq, reinterpret_cast<float*>(ws + L.i4part), i4part_floats(s)}
                                : Int4Scratch{nullptr, nullptr, nullptr};
@@ -1588,6 +1794,140 @@ int moe_quantize_int4(const float* w, int64_t rows, int32_t K, uint8_t* q, void*
                                                                  reinterpret_cast<__nv_bfloat16*>(scales));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
+}
+
+int moe_quantize_int8(const void* x, int32_t dtype, int64_t rows, int32_t K, int8_t* q, float* scales,
+                      moe_stream_t stream) {
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32) return MOE_INVALID_ARGUMENT;
+  if (rows < 0 || rows >= (1ll << 31) || K < 16 || K % 16 != 0) return MOE_UNSUPPORTED_SHAPE;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !scales || !aligned16(x) || !aligned16(q) || (reinterpret_cast<uintptr_t>(scales) & 3u))
+    return MOE_INVALID_ARGUMENT;
+  if (dtype == MOE_DTYPE_BF16)
+    return launch_quant_rows(reinterpret_cast<const __nv_bfloat16*>(x), rows, K, q, scales, stream);
+  return launch_quant_rows(reinterpret_cast<const float*>(x), rows, K, q, scales, stream);
+}
+
+int moe_permute_int8(const moe_shape* s, const void* x, const int32_t* topk_idx, int32_t* slot_pos,
+                     uint8_t* drop_mask, int32_t* counts, int32_t* kept, int32_t* offsets, int32_t* row_src,
+                     int8_t* xq_perm, float* xs_perm, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+  int rc = check_shape(s);
+  if (rc) return rc;
+  if (!x || !topk_idx || !slot_pos || !kept || !offsets || !xq_perm || !xs_perm || !workspace)
+    return MOE_INVALID_ARGUMENT;
+  if (!aligned16(x) || !aligned16(xq_perm) || !aligned16(xs_perm) || !aligned16(workspace))
+    return MOE_INVALID_ARGUMENT;
+  const Workspace L = ws_layout(s);
+  if (ws_bytes < L.total) return MOE_WORKSPACE_TOO_SMALL;
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  int32_t* cnt = reinterpret_cast<int32_t*>(ws + L.cnt);
+  int32_t* cts = counts ? counts : reinterpret_cast<int32_t*>(ws + L.counts);
+  const int nchunks = (int)cdiv(s->T, kChunk);
+  MOE_LAUNCH((k_chunk_hist), nchunks, 256, s->E * sizeof(int), stream, topk_idx, cnt, (int)s->T, s->E, s->k);
+  MOE_LAUNCH_CHECK();
+  rc = launch_scan(s, cnt, nullptr, cts, nullptr, nullptr, stream);
+  if (rc) return rc;
+  rc = launch_scatter(s, x, topk_idx, cnt, cts, slot_pos, drop_mask, row_src, nullptr, kept, offsets, stream, false);
+  if (rc) return rc;
+  return launch_quant_slots(s, x, slot_pos, xq_perm, xs_perm, nullptr, nullptr, stream);
+}
+
+// Limits shared by moe_expert_ffn_int8 and its size query.
+static int check_ffn_int8(const moe_shape* s, int32_t n_groups, int32_t hidden, int64_t R) {
+  int rc = check_shape(s);
+  if (rc) return rc;
+  if (s->wfmt != MOE_WFMT_INT8) return MOE_INVALID_ARGUMENT;
+  if (n_groups < 1 || n_groups > kMaxGroupsSmem || R < 0 || R >= (1ll << 31) - 256) return MOE_INVALID_ARGUMENT;
+  if (hidden < 16 || hidden % 16 != 0 || hidden > 65536) return MOE_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+int moe_expert_ffn_int8_workspace_size(const moe_shape* s, int32_t hidden, int64_t R, size_t* bytes) {
+  int rc = check_ffn_int8(s, 1, hidden, R);
+  if (rc) return rc;
+  if (!bytes) return MOE_INVALID_ARGUMENT;
+  *bytes = int8_ffn_bytes(hidden, R);
+  return MOE_OK;
+}
+
+int moe_expert_ffn_int8(const moe_shape* s, int32_t n_groups, int32_t hidden, int64_t R, const int8_t* xq,
+                        const float* xs, const int32_t* group_start, const int32_t* group_rows, const int8_t* w13,
+                        const float* s13, const int8_t* w2, const float* s2, void* y, void* workspace,
+                        size_t ws_bytes, moe_stream_t stream) {
+  int rc = check_ffn_int8(s, n_groups, hidden, R);
+  if (rc) return rc;
+  if ((group_start == nullptr) != (group_rows == nullptr)) return MOE_INVALID_ARGUMENT;
+  if (group_start == nullptr && n_groups != 1) return MOE_INVALID_ARGUMENT;
+  if (R == 0) return MOE_OK;
+  if (!xq || !xs || !w13 || !s13 || !w2 || !s2 || !y || !workspace) return MOE_INVALID_ARGUMENT;
+  if (!aligned16(xq) || !aligned16(xs) || !aligned16(w13) || !aligned16(s13) || !aligned16(w2) || !aligned16(s2) ||
+      !aligned16(y) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return MOE_INVALID_ARGUMENT;
+  if (ws_bytes < int8_ffn_bytes(hidden, R)) return MOE_WORKSPACE_TOO_SMALL;
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  uint8_t* hq = ws + align256((size_t)R * hidden * 2);
+  float* hs = reinterpret_cast<float*>(hq + align256((size_t)R * hidden));
+  return int8_ffn(s, hidden, R, xq, xs, group_start, group_rows, n_groups, w13, s13, w2, s2, ws, hq, hs, y, stream);
+}
+
+int moe_combine_backward(const moe_shape* s, const void* dout, const void* y_perm, const int32_t* slot_pos,
+                         const float* topk_w, const int32_t* kept, void* dy_perm, float* dtopk_w,
+                         moe_stream_t stream) {
+  int rc = check_shape(s);
+  if (rc) return rc;
+  if (!dout || !slot_pos || !topk_w || (!dy_perm && !dtopk_w) || (dtopk_w && !y_perm)) return MOE_INVALID_ARGUMENT;
+  if (kept && (!dy_perm || s->capacity == 0)) return MOE_INVALID_ARGUMENT;
+  if (!aligned16(dout) || !aligned16(y_perm) || !aligned16(dy_perm)) return MOE_INVALID_ARGUMENT;
+  const __nv_bfloat16* g = reinterpret_cast<const __nv_bfloat16*>(dout);
+  const __nv_bfloat16* y = reinterpret_cast<const __nv_bfloat16*>(y_perm);
+  __nv_bfloat16* dy = reinterpret_cast<__nv_bfloat16*>(dy_perm);
+  const int R = (int)grouped_rows(s);
+  // a CTA per token where a warp per token would leave SMs without work
+  const bool wide = s->T < 8ll * num_sms() && s->d > 256;
+  const unsigned tok = (unsigned)(wide ? s->T : cdiv(s->T, 8));
+  const unsigned pad = kept ? (unsigned)(s->E * cdiv(s->capacity, kPadRows)) : 0u;
+#define MOE_CBWD(N_)                                                                                              \
+  if (s->k <= N_) {                                                                                               \
+    if (wide)                                                                                                     \
+      MOE_LAUNCH((k_combine_bwd<N_, 8>), tok + pad, 256, 0, stream, g, y, slot_pos, topk_w, dy, dtopk_w,          \
+                 (int)s->T, s->d, s->k, R, tok, kept, s->capacity);                                               \
+    else                                                                                                          \
+      MOE_LAUNCH((k_combine_bwd<N_, 1>), tok + pad, 256, 0, stream, g, y, slot_pos, topk_w, dy, dtopk_w,          \
+                 (int)s->T, s->d, s->k, R, tok, kept, s->capacity);                                               \
+    MOE_LAUNCH_CHECK();                                                                                           \
+    return MOE_OK;                                                                                                \
+  }
+  MOE_CBWD(2) MOE_CBWD(4) MOE_CBWD(8) MOE_CBWD(16)
+#undef MOE_CBWD
+  return MOE_UNSUPPORTED_SHAPE;
+}
+
+int moe_permute_backward(const moe_shape* s, const void* dx_perm, int32_t in_dtype, const int32_t* slot_pos,
+                         const void* add, void* dx, int32_t out_dtype, moe_stream_t stream) {
+  int rc = check_shape(s);
+  if (rc) return rc;
+  auto known = [](int32_t t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; };
+  if (!known(in_dtype) || !known(out_dtype)) return MOE_INVALID_ARGUMENT;
+  if (!dx_perm || !slot_pos || !dx) return MOE_INVALID_ARGUMENT;
+  if (!aligned16(dx_perm) || !aligned16(add) || !aligned16(dx)) return MOE_INVALID_ARGUMENT;
+  const int R = (int)grouped_rows(s);
+  const unsigned blocks = (unsigned)cdiv(s->T * (long long)(s->d / 8), 256);
+#define MOE_PBWD_T(N_, I_, O_)                                                                                    \
+  MOE_LAUNCH((k_permute_bwd<N_, I_, O_>), blocks, 256, 0, stream, reinterpret_cast<const I_*>(dx_perm), slot_pos, \
+             reinterpret_cast<const O_*>(add), reinterpret_cast<O_*>(dx), (int)s->T, s->d, s->k, R)
+#define MOE_PBWD(N_)                                                                                              \
+  if (s->k <= N_) {                                                                                               \
+    if (in_dtype == MOE_DTYPE_BF16 && out_dtype == MOE_DTYPE_BF16) MOE_PBWD_T(N_, __nv_bfloat16, __nv_bfloat16);  \
+    else if (in_dtype == MOE_DTYPE_BF16) MOE_PBWD_T(N_, __nv_bfloat16, float);                                    \
+    else if (out_dtype == MOE_DTYPE_BF16) MOE_PBWD_T(N_, float, __nv_bfloat16);                                   \
+    else MOE_PBWD_T(N_, float, float);                                                                            \
+    MOE_LAUNCH_CHECK();                                                                                           \
+    return MOE_OK;                                                                                                \
+  }
+  MOE_PBWD(2) MOE_PBWD(4) MOE_PBWD(8) MOE_PBWD(16)
+#undef MOE_PBWD
+#undef MOE_PBWD_T
+  return MOE_UNSUPPORTED_SHAPE;
 }
 
 int moe_get_status(moe_stream_t stream, int32_t* device_status, uint32_t* site) {
