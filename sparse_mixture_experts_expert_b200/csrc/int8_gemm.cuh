@@ -11,11 +11,14 @@
 // Structure as k_grouped_gemm: persistent CTAs, warp 0 feeds A and B tiles of 128 bytes of K by TMA into a ring,
 // warp 1 issues tcgen05.mma (M = 128, or 256 over a CTA pair; four MMAs of K = 32 per stage), and the epilogue drains
 // one accumulator while the next one fills.  A k-step holds twice the inputs of a bf16 one for the same bytes and the
-// same MMA time, so a tile's main loop takes half as long and the epilogue weighs twice as much: eight epilogue warps
-// (two per TMEM quarter, each on half of the columns) instead of four.
-// Row tiles that a group does not fill load their rows in boxes of 32, no more than it has: with a handful of rows an
-// expert (decode) the weights are then nearly all that moves.  Shared memory behind those rows holds whatever it
-// held; integer products of it are finite and stay in rows that the epilogue does not store.
+// same MMA time, so a tile's main loop takes half as long and the epilogue weighs twice as much: sixteen epilogue warps
+// (four per TMEM quarter, each on a quarter of the columns) instead of four, and rows stored straight from the
+// registers in whole 32-byte sectors instead of through shared memory.
+// Row tiles of at most 64 rows load them in boxes of 32, no more than the group has: with a handful of rows an expert
+// (decode) the weights are then nearly all that moves.  Shared memory behind those rows holds whatever it held; integer
+// products of it are finite and stay in rows that the epilogue does not store.  Fuller tiles take one box of 128 rows
+// (four of 32 made the gate/up kernel of 16384 rows, 768 -> 4096, 168 us instead of 138: the copy engine's work goes
+// by the box).
 #pragma once
 
 #include "gemm_tc.cuh"
@@ -39,22 +42,20 @@ struct I8Params {
 };
 
 constexpr int kI8BK = 128;                      // codes per k-step: one 128-byte swizzle row
-constexpr int kI8ABox = 32;                     // rows per A box
-constexpr int kI8Threads = 384;
-constexpr int kI8EpiWarps = 8;
-constexpr int kI8EpiW = 32;                     // columns a warp stages per round
-constexpr int kI8EpiRow = kI8EpiW + 8;          // padded staging row (bf16)
-constexpr int kI8EpiBytes = kI8EpiWarps * 32 * kI8EpiRow * 2;
+constexpr int kI8ABox = 32;                     // rows per A box of a tile of at most kI8Few rows, else kBM
+constexpr int kI8Few = 64;
+constexpr int kI8EpiWarps = 16;
+constexpr int kI8Threads = (4 + kI8EpiWarps) * 32;
 
 template <int BN, int CG>
 struct I8Cfg {
   static constexpr int kABytes = kBM * kI8BK;
   static constexpr int kBBytes = (CG == 2 ? BN / 2 : BN) * kI8BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kBudget = 216 * 1024 - 1024 - kI8EpiBytes;
+  static constexpr int kBudget = 215 * 1024 - 1024;
   static constexpr int kStages = kBudget / kStageBytes > 8 ? 8 : kBudget / kStageBytes;
   static constexpr int kTmemCols = 2 * BN;      // two accumulators (128, 256 or 512 columns)
-  static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kI8EpiBytes;
+  static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes;
 };
 
 // Instruction descriptor, kind::i8: D s32, A and B signed 8-bit, both K-major, M x N.
@@ -83,6 +84,44 @@ __device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint
         "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// 16 bf16 values of a row: one 32-byte sector per lane in one store where the output lies on 32-byte boundaries
+// (`wide`, the same for the whole output: its rows are multiples of 32 bytes), else two of 16 bytes.
+__device__ __forceinline__ void st_row16(void* p, const uint32_t (&o)[8], bool wide) {
+  if (!wide) {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+               "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+               : "memory");
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// act(g) with few instructions.  SiLU: g / (1 + exp(-g)).  GELU: g Phi(g) = max(g, 0) - |g| Q(|g|) with the normal
+// tail Q(a) = erfc(a / sqrt 2) / 2 by Abramowitz & Stegun 7.1.26 (the factor 1/2 and the sqrt 2 folded into its
+// coefficients); the tail form does not cancel for negative g.
+template <int MODE>
+__device__ __forceinline__ float i8_act(float g) {
+  if (MODE == kModeSwiGLU) return g * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * g));
+  const float a = fabsf(g);
+  const float t = rcp_approx(fmaf(0.3275911f * 0.7071067811865476f, a, 1.0f));
+  const float poly = t * (0.5f * 0.254829592f +
+                          t * (-0.5f * 0.284496736f +
+                               t * (0.5f * 1.421413741f + t * (-0.5f * 1.453152027f + t * (0.5f * 1.061405429f)))));
+  const float e = ex2_approx(-0.7213475204444817f * (g * g));
+  return fmaf(-a, poly * e, fmaxf(g, 0.0f));
 }
 
 // First row and number of rows of group g, kept inside [0, R).
@@ -137,7 +176,8 @@ __device__ __forceinline__ int i8_find_group(const int* prefix, int G, int mt) {
 
 template <int MODE, int BN, int CG>
 __global__ void __launch_bounds__(kI8Threads, 1)
-    k_int8_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const I8Params p) {
+    k_int8_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAFew,
+                const __grid_constant__ CUtensorMap tmB, const I8Params p) {
   pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
   using Cfg = I8Cfg<BN, CG>;
   constexpr bool kGLU = MODE == kModeSwiGLU || MODE == kModeGeGLU;
@@ -155,7 +195,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   __shared__ int s_prefix[kMaxGroupsSmem + 1];
   __shared__ int s_gstart[kMaxGroupsSmem];
   __shared__ int s_grows[kMaxGroupsSmem];
-  __shared__ __align__(16) float s_scale[kI8EpiWarps][kGLU ? OUTN : OUTN / 2];
+  constexpr int PARTS = OUTN >= 64 ? 4 : OUTN / 16;   // epilogue warps per TMEM quarter that have columns
+  constexpr int CW = OUTN / PARTS;                    // output columns of such a warp, in chunks of 16
+  __shared__ __align__(16) float s_scale[4 * PARTS][kGLU ? 2 * CW : CW];
 
   const int warp = warp_id(), lane = lane_id();
   const int crank = kPair ? (int)cluster_ctarank() : 0;   // 0 = leader of the pair
@@ -168,11 +210,12 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   if (warp == 2) i8_group_table(p, TM, s_prefix, s_gstart, s_grows);
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(&bar_full[s], 1); mbar_init(&bar_empty[s], 1); }
-    for (int a = 0; a < 2; ++a) { mbar_init(&bar_tfull[a], 1); mbar_init(&bar_tempty[a], CG * kI8EpiWarps); }
+    for (int a = 0; a < 2; ++a) { mbar_init(&bar_tfull[a], 1); mbar_init(&bar_tempty[a], CG * 4 * PARTS); }
     mbar_init(&bar_final, 1);
     s_abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmAFew);
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
@@ -200,7 +243,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     row0 = s_gstart[g] + m_tile + crank * kBM;
     rows_left = s_grows[g] - m_tile;
   };
-  auto boxes = [](int rows) { return (max(0, min(kBM, rows)) + kI8ABox - 1) / kI8ABox; };
+  // rows that a CTA with `rows` rows of its tile left loads
+  auto loaded = [](int rows) {
+    return rows <= 0 ? 0 : rows > kI8Few ? kBM : (rows + kI8ABox - 1) / kI8ABox * kI8ABox;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
@@ -211,9 +257,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       for (long long tile = unit; tile < total && !s_abort; tile += n_units) {
         int g, row0, rows_left, n0;
         locate(tile, g, row0, rows_left, n0);
-        const int na = boxes(rows_left - crank * kBM);
-        const int na_all = kPair ? boxes(rows_left) + boxes(rows_left - kBM) : na;
-        const uint32_t bytes = (uint32_t)(na_all * kI8ABox * kI8BK + CG * Cfg::kBBytes);
+        const int na = loaded(rows_left - crank * kBM);
+        const int na_all = kPair ? loaded(rows_left) + loaded(rows_left - kBM) : na;
+        const uint32_t bytes = (uint32_t)(na_all * kI8BK + CG * Cfg::kBBytes);
         bool ok = true;
         for (int kb = 0; kb < nk; ++kb) {
           uint8_t* a_s = smem + (size_t)stage * Cfg::kStageBytes;
@@ -224,13 +270,17 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           if (crank == 0) mbar_arrive_expect_tx(&bar_full[stage], bytes);
           if (kPair) {
             const uint32_t fb = mapa_shared(smem_u32(&bar_full[stage]), 0);
-            for (int i = 0; i < na; ++i)
-              tma_load_2d_pair(a_s + i * (kI8ABox * kI8BK), &tmA, fb, kb * kI8BK, row0 + i * kI8ABox);
+            if (na == kBM) tma_load_2d_pair(a_s, &tmA, fb, kb * kI8BK, row0);
+            else
+              for (int i = 0; i < na; i += kI8ABox)
+                tma_load_2d_pair(a_s + i * kI8BK, &tmAFew, fb, kb * kI8BK, row0 + i);
             const int brow = kGLU ? (crank == 0 ? n0 : p.up_row0 + n0) : n0 + crank * (BN / 2);
             tma_load_3d_pair(b_s, &tmB, fb, kb * kI8BK, brow, g);
           } else {
-            for (int i = 0; i < na; ++i)
-              tma_load_2d(a_s + i * (kI8ABox * kI8BK), &tmA, &bar_full[stage], kb * kI8BK, row0 + i * kI8ABox);
+            if (na == kBM) tma_load_2d(a_s, &tmA, &bar_full[stage], kb * kI8BK, row0);
+            else
+              for (int i = 0; i < na; i += kI8ABox)
+                tma_load_2d(a_s + i * kI8BK, &tmAFew, &bar_full[stage], kb * kI8BK, row0 + i);
             tma_load_3d(b_s, &tmB, &bar_full[stage], kb * kI8BK, n0, g);
             if (kGLU)
               tma_load_3d(b_s + (BN / 2) * kI8BK, &tmB, &bar_full[stage], kb * kI8BK, p.up_row0 + n0, g);
@@ -289,51 +339,44 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       mbar_wait(&bar_final, 0, p.wait_limit_ns, &dummy, 0x0505);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 4 + 4 * PARTS) {
     // ------------------------------------------------ epilogue
     const int ew = warp - 4;
     const int q = warp & 3;                 // TMEM lane quarter: this warp's 32 accumulator rows
-    constexpr int HALF = OUTN / 2;          // output columns of this warp
-    const int c_base = (ew >> 2) * HALF;
-    constexpr int OUTW = HALF < kI8EpiW ? HALF : kI8EpiW;
-    constexpr int ROUNDS = HALF / OUTW;
-    constexpr int NCH = OUTW / 16;
-    constexpr int LPR = OUTW / 8;           // lanes per staged row in the copy-out
-    constexpr int RPI = 32 / LPR;           // rows per copy-out iteration
-    __nv_bfloat16* stg =
-        reinterpret_cast<__nv_bfloat16*>(smem + (size_t)S * Cfg::kStageBytes) + ew * 32 * kI8EpiRow;
+    const int c_base = (ew >> 2) * CW;      // this warp's first output column in the tile
     float* scl = s_scale[ew];
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (long long tile = unit; tile < total && !s_abort; tile += n_units) {
       int g, row0, rows_left, n0;
       locate(tile, g, row0, rows_left, n0);
-      const int rows_valid = max(0, min(kBM, rows_left - crank * kBM));
+      const int row = q * 32 + lane;
+      const bool live = row < rows_left - crank * kBM;
       // this warp's channel scales (gate, then up) and this lane's token scale, while the MMAs run
       {
         const float* bs = p.b_scale + (size_t)g * p.b_rows;
-        for (int c = lane; c < HALF; c += 32) {
+        for (int c = lane; c < CW; c += 32) {
           const int col = n0 + c_base + c;
           scl[c] = col < p.N ? bs[col] : 0.f;
-          if (kGLU) scl[HALF + c] = col < p.N ? bs[p.up_row0 + col] : 0.f;
+          if (kGLU) scl[CW + c] = col < p.N ? bs[p.up_row0 + col] : 0.f;
         }
       }
-      const float sx = q * 32 + lane < rows_valid ? p.a_scale[(long long)row0 + q * 32 + lane] : 0.f;
+      const float sx = live ? p.a_scale[(long long)row0 + row] : 0.f;
+      __nv_bfloat16* out = p.out + ((long long)row0 + row) * p.N + n0 + c_base;
+      const int cols = p.N - n0 - c_base;   // N is a multiple of 16: whole chunks
       __syncwarp();
       if (!mbar_wait(&bar_tfull[acc], acc_phase, p.wait_limit_ns, &s_abort, 0x0506)) break;
       tc_fence_after();
       const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN + c_base);
-#pragma unroll 1
-      for (int rd = 0; rd < ROUNDS; ++rd) {
-        uint32_t v[NCH][16];
-        uint32_t u[kGLU ? NCH : 1][16];
 #pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-          tmem_ld16(t_row + rd * OUTW + ch * 16, v[ch]);
-          if (kGLU) tmem_ld16(t_row + OUTN + rd * OUTW + ch * 16, u[kGLU ? ch : 0]);
-        }
+      for (int c0 = 0; c0 < CW; c0 += 16) {
+        uint32_t v[16];
+        uint32_t u[kGLU ? 16 : 1];
+        tmem_ld16(t_row + c0, v);
+        if constexpr (kGLU) tmem_ld16(t_row + OUTN + c0, u);
         tmem_ld_wait();
-        if (rd == ROUNDS - 1) {   // the accumulator is drained: one arrival per epilogue warp (on the leader)
+        if (c0 + 16 == CW) {   // the accumulator is drained: one arrival per epilogue warp (on the leader)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -341,45 +384,24 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             else mbar_arrive(&bar_tempty[acc]);
           }
         }
+        uint32_t o[8];
 #pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-          uint32_t o[8];
+        for (int i = 0; i < 16; i += 4) {
+          const float4 sg = *reinterpret_cast<const float4*>(scl + c0 + i);
+          const float gs[4] = {sg.x, sg.y, sg.z, sg.w};
+          float f[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = rd * OUTW + ch * 16 + 4 * i;
-            const float4 sg = *reinterpret_cast<const float4*>(scl + c);
-            float f[4];
-            const float gs[4] = {sg.x, sg.y, sg.z, sg.w};
+          for (int j = 0; j < 4; ++j) f[j] = (float)(int)v[i + j] * sx * gs[j];
+          if constexpr (kGLU) {
+            const float4 su = *reinterpret_cast<const float4*>(scl + CW + c0 + i);
+            const float us[4] = {su.x, su.y, su.z, su.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = (float)(int)v[ch][4 * i + j] * sx * gs[j];
-            if (kGLU) {
-              const float4 su = *reinterpret_cast<const float4*>(scl + HALF + c);
-              const float us[4] = {su.x, su.y, su.z, su.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float up = (float)(int)u[kGLU ? ch : 0][4 * i + j] * sx * us[j];
-                f[j] = (MODE == kModeSwiGLU ? act_silu(f[j]) : act_gelu(f[j])) * up;
-              }
-            }
-            o[2 * i] = pack_bf16x2(f[0], f[1]);
-            o[2 * i + 1] = pack_bf16x2(f[2], f[3]);
+            for (int j = 0; j < 4; ++j) f[j] = i8_act<MODE>(f[j]) * ((float)(int)u[i + j] * sx * us[j]);
           }
-          uint4* sp = reinterpret_cast<uint4*>(stg + lane * kI8EpiRow + ch * 16);
-          sp[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          sp[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          o[i / 2] = pack_bf16x2(f[0], f[1]);
+          o[i / 2 + 1] = pack_bf16x2(f[2], f[3]);
         }
-        __syncwarp();
-        const int cb = (lane % LPR) * 8;
-        const int col = n0 + c_base + rd * OUTW + cb;
-#pragma unroll
-        for (int it = 0; it < 32 / RPI; ++it) {
-          const int rr = it * RPI + lane / LPR;
-          if (q * 32 + rr < rows_valid && col < p.N) {
-            const uint4 val = *reinterpret_cast<const uint4*>(stg + rr * kI8EpiRow + cb);
-            *reinterpret_cast<uint4*>(p.out + ((long long)row0 + q * 32 + rr) * p.N + col) = val;
-          }
-        }
-        __syncwarp();
+        if (live && c0 < cols) st_row16(out + c0, o, wide);
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
@@ -395,7 +417,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 }
 
 // Codes and scales of the rows that the groups hold (h between the two products); rows outside every group are not
-// read.  A row per warp (TPR 32) or per CTA (TPR 256), the filled rows dealt over a fixed grid.
+// read.  A row per TPR threads, the filled rows dealt over a fixed grid.
 template <int TPR>
 __global__ void __launch_bounds__(256) k_quant_groups(const __nv_bfloat16* __restrict__ x, const I8Params p,
                                                       int8_t* __restrict__ q, float* __restrict__ scale) {
@@ -409,14 +431,16 @@ __global__ void __launch_bounds__(256) k_quant_groups(const __nv_bfloat16* __res
   const int K = p.K;
   const int total = s_prefix[p.n_groups];
   constexpr int RPC = 256 / TPR;   // rows per CTA and step
-  for (long long i = (long long)blockIdx.x * RPC + (TPR == 32 ? warp_id() : 0); i < total;
-       i += (long long)gridDim.x * RPC) {
-    const int g = i8_find_group(s_prefix, p.n_groups, (int)i);
-    const size_t r = (size_t)(s_gstart[g] + (int)i - s_prefix[g]);
-    const float s = quant_row<TPR>(x + r * K, K, s_max, [&](int c, uint2 v) {
+  const int sub = (int)threadIdx.x / TPR;
+  for (long long i0 = (long long)blockIdx.x * RPC; i0 < total; i0 += (long long)gridDim.x * RPC) {
+    const bool on = i0 + sub < total;
+    const int i = (int)(on ? i0 + sub : i0);
+    const int g = i8_find_group(s_prefix, p.n_groups, i);
+    const size_t r = (size_t)(s_gstart[g] + i - s_prefix[g]);
+    const float s = quant_row<TPR>(x + r * K, K, on, s_max, [&](int c, uint2 v) {
       reinterpret_cast<uint2*>(q + r * K)[c] = v;
     });
-    if ((TPR == 32 ? lane_id() : (int)threadIdx.x) == 0) scale[r] = s;
+    if (on && (int)threadIdx.x % TPR == 0) scale[r] = s;
   }
 }
 

@@ -76,28 +76,32 @@ __device__ __forceinline__ uint2 quant_vec(const RawVec<T>& v, float r) {
                                quant_code(v.at(7), r)));
 }
 
-// One row by TPR threads (a warp, or the CTA's 256): maximum, then codes handed to put(vector index, 8 codes) and
-// the scale returned.  Rows longer than TPR * kQuantVec vectors are read a second time past that.
+// One row by TPR threads (8 or 32 lanes of a warp, or the CTA's 256): maximum, then codes handed to put(vector index,
+// 8 codes); returns the scale.  Every thread of the warp (or CTA) takes part; with on == false it reads and puts
+// nothing.  Rows longer than TPR * kQuantVec vectors are read a second time past that.
 template <int TPR, typename T, typename Put>
-__device__ __forceinline__ float quant_row(const T* __restrict__ x, int K, uint32_t* s_max, Put put) {
-  const int nvec = K >> 3;
-  const int th = TPR == 32 ? lane_id() : (int)threadIdx.x;
+__device__ __forceinline__ float quant_row(const T* __restrict__ x, int K, bool on, uint32_t* s_max, Put put) {
+  const int nvec = on ? K >> 3 : 0;
+  const int th = (int)threadIdx.x % TPR;
   RawVec<T> v[kQuantVec];
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kQuantVec; ++i) {
-    const int c = th + i * TPR;
-    if (c < nvec) {
-      v[i].load(x + 8 * c);
-      m = max(m, v[i].top());
-    }
-  }
+  for (int i = 0; i < kQuantVec; ++i)
+    if (th + i * TPR < nvec) v[i].load(x + 8 * (th + i * TPR));
+#pragma unroll
+  for (int i = 0; i < kQuantVec; ++i)
+    if (th + i * TPR < nvec) m = max(m, v[i].top());
   for (int c = th + kQuantVec * TPR; c < nvec; c += TPR) {
     RawVec<T> u;
     u.load(x + 8 * c);
     m = max(m, u.top());
   }
-  m = __reduce_max_sync(0xffffffffu, m);
+  if (TPR == 8) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  } else {
+    m = __reduce_max_sync(0xffffffffu, m);
+  }
   if (TPR > 32) {
     if (lane_id() == 0) s_max[warp_id()] = m;
     __syncthreads();
@@ -109,10 +113,8 @@ __device__ __forceinline__ float quant_row(const T* __restrict__ x, int K, uint3
   float s, r;
   quant_scale(__uint_as_float(m), s, r);
 #pragma unroll
-  for (int i = 0; i < kQuantVec; ++i) {
-    const int c = th + i * TPR;
-    if (c < nvec) put(c, quant_vec(v[i], r));
-  }
+  for (int i = 0; i < kQuantVec; ++i)
+    if (th + i * TPR < nvec) put(th + i * TPR, quant_vec(v[i], r));
   for (int c = th + kQuantVec * TPR; c < nvec; c += TPR) {
     RawVec<T> u;
     u.load(x + 8 * c);
@@ -121,18 +123,18 @@ __device__ __forceinline__ float quant_row(const T* __restrict__ x, int K, uint3
   return s;
 }
 
-// Rows 0 .. rows-1 of x [rows, K]; one row per warp (TPR 32) or per CTA (TPR 256).
+// Rows 0 .. rows-1 of x [rows, K], 256 / TPR rows per CTA.
 template <int TPR, typename T>
 __global__ void __launch_bounds__(256) k_quant_rows(const T* __restrict__ x, long long rows, int K,
                                                     int8_t* __restrict__ q, float* __restrict__ scale) {
   pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
   __shared__ uint32_t s_max[8];
-  const long long r = TPR == 32 ? (long long)blockIdx.x * 8 + warp_id() : (long long)blockIdx.x;
-  if (r >= rows) return;
-  const float s = quant_row<TPR>(x + r * K, K, s_max, [&](int c, uint2 v) {
+  const long long r = (long long)blockIdx.x * (256 / TPR) + (int)threadIdx.x / TPR;
+  const bool on = r < rows;
+  const float s = quant_row<TPR>(x + r * K, K, on, s_max, [&](int c, uint2 v) {
     reinterpret_cast<uint2*>(q + r * K)[c] = v;
   });
-  if ((TPR == 32 ? lane_id() : (int)threadIdx.x) == 0) scale[r] = s;
+  if (on && (int)threadIdx.x % TPR == 0) scale[r] = s;
 }
 
 // The dispatch: token t's row is read once, quantised, and its codes and scale written to the grouped row of each of
@@ -144,21 +146,21 @@ __global__ void __launch_bounds__(256) k_quant_slots(const __nv_bfloat16* __rest
                                                      int8_t* __restrict__ q_tok, float* __restrict__ s_tok) {
   pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
   __shared__ uint32_t s_max[8];
-  const long long t = TPR == 32 ? (long long)blockIdx.x * 8 + warp_id() : (long long)blockIdx.x;
-  if (t >= T) return;
+  const long long t = (long long)blockIdx.x * (256 / TPR) + (int)threadIdx.x / TPR;
+  const bool on = t < T;
   int p[KMAX];
 #pragma unroll
   for (int j = 0; j < KMAX; ++j) {
-    p[j] = j < k ? slot_pos[t * k + j] : -1;
+    p[j] = on && j < k ? slot_pos[t * k + j] : -1;
     if ((unsigned)p[j] >= (unsigned)R) p[j] = -1;
   }
-  const float s = quant_row<TPR>(x + t * d, d, s_max, [&](int c, uint2 v) {
+  const float s = quant_row<TPR>(x + t * d, d, on, s_max, [&](int c, uint2 v) {
 #pragma unroll
     for (int j = 0; j < KMAX; ++j)
       if (p[j] >= 0) reinterpret_cast<uint2*>(q + (size_t)p[j] * d)[c] = v;
     if (q_tok != nullptr) reinterpret_cast<uint2*>(q_tok + t * d)[c] = v;
   });
-  if ((TPR == 32 ? lane_id() : (int)threadIdx.x) == 0) {
+  if (on && (int)threadIdx.x % TPR == 0) {
 #pragma unroll
     for (int j = 0; j < KMAX; ++j)
       if (p[j] >= 0) scale[p[j]] = s;

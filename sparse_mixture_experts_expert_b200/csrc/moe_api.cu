@@ -13,6 +13,7 @@
 #include "expert_fused.cuh"
 #include "gemm_tc.cuh"
 #include "int4_gemm.cuh"
+#include "int8_fused.cuh"
 #include "int8_gemm.cuh"
 #include "int8_quant.cuh"
 #include "permute.cuh"
@@ -699,7 +700,7 @@ static int make_map_i8(CUtensorMap* m, const void* base, int rank, const cuuint6
 }
 
 template <int MODE, int BN, int CG>
-static int launch_i8_t(const CUtensorMap& ta, const CUtensorMap& tb, const I8Params& p, long long ub_mtiles,
+static int launch_i8_t(const CUtensorMap& ta, const CUtensorMap& taf, const CUtensorMap& tb, const I8Params& p, long long ub_mtiles,
                        cudaStream_t st) {
   using Cfg = I8Cfg<BN, CG>;
   constexpr int OUTN = (MODE == kModeSwiGLU || MODE == kModeGeGLU) ? BN / 2 : BN;
@@ -713,7 +714,7 @@ static int launch_i8_t(const CUtensorMap& ta, const CUtensorMap& tb, const I8Par
   const long long tiles = ub_mtiles * cdiv(p.N, OUTN);
   const int units = (int)std::max<long long>(1, std::min<long long>(num_sms() / CG, tiles));
   MOE_CUDA_TRY(launch_pdl(k_int8_gemm<MODE, BN, CG>, dim3((unsigned)(CG * units)), dim3(kI8Threads), Cfg::kSmemBytes,
-                          st, (unsigned)CG, ta, tb, p));
+                          st, (unsigned)CG, ta, taf, tb, p));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -726,10 +727,12 @@ static int int8_gemm(int mode, const void* A, const float* a_scale, long long R,
   const long long ub_m = grows ? (R / kBM + n_groups) : cdiv(R, kBM);
   const int BN = pick_bn(glu, N, ub_m);
   const bool pair = use_pair_gemm(mode, BN, R, n_groups, allow_pair);
-  CUtensorMap ta, tb;
+  CUtensorMap ta, taf, tb;
   const cuuint64_t da[2] = {(cuuint64_t)K, (cuuint64_t)R};
   const cuuint64_t db[3] = {(cuuint64_t)K, (cuuint64_t)b_rows, (cuuint64_t)n_groups};
-  int rc = make_map_i8(&ta, A, 2, da, kI8ABox);
+  int rc = make_map_i8(&ta, A, 2, da, kBM);
+  if (rc) return rc;
+  rc = make_map_i8(&taf, A, 2, da, kI8ABox);
   if (rc) return rc;
   rc = make_map_i8(&tb, B, 3, db, (glu || pair) ? BN / 2 : BN);
   if (rc) return rc;
@@ -749,12 +752,12 @@ static int int8_gemm(int mode, const void* A, const float* a_scale, long long R,
   const long long TM = (long long)kBM * (pair ? 2 : 1);
   const long long ub = grows ? (R / TM + n_groups) : cdiv(R, TM);
   if (pair) {
-    if (mode == kModePlain) return launch_i8_t<kModePlain, 256, 2>(ta, tb, p, ub, st);
-    if (mode == kModeSwiGLU) return launch_i8_t<kModeSwiGLU, 256, 2>(ta, tb, p, ub, st);
-    return launch_i8_t<kModeGeGLU, 256, 2>(ta, tb, p, ub, st);
+    if (mode == kModePlain) return launch_i8_t<kModePlain, 256, 2>(ta, taf, tb, p, ub, st);
+    if (mode == kModeSwiGLU) return launch_i8_t<kModeSwiGLU, 256, 2>(ta, taf, tb, p, ub, st);
+    return launch_i8_t<kModeGeGLU, 256, 2>(ta, taf, tb, p, ub, st);
   }
 #define MOE_I8_CASE(M_, BN_) \
-  if (mode == M_ && BN == BN_) return launch_i8_t<M_, BN_, 1>(ta, tb, p, ub, st);
+  if (mode == M_ && BN == BN_) return launch_i8_t<M_, BN_, 1>(ta, taf, tb, p, ub, st);
   MOE_I8_CASE(kModePlain, 256) MOE_I8_CASE(kModePlain, 128) MOE_I8_CASE(kModePlain, 64)
   MOE_I8_CASE(kModeSwiGLU, 256) MOE_I8_CASE(kModeSwiGLU, 128) MOE_I8_CASE(kModeSwiGLU, 64)
   MOE_I8_CASE(kModeGeGLU, 256) MOE_I8_CASE(kModeGeGLU, 128) MOE_I8_CASE(kModeGeGLU, 64)
@@ -762,14 +765,18 @@ static int int8_gemm(int mode, const void* A, const float* a_scale, long long R,
   return MOE_UNSUPPORTED_SHAPE;
 }
 
-// Codes and scales of x [rows, K]: a row per warp up to 1024 columns (four 8-element vectors a lane stay in
-// registers), else a row per CTA.
+// Threads that quantise a row: as few as hold it in registers (four 8-element vectors each), so that every thread
+// has several loads in flight: 8 lanes up to 256 columns, a warp up to 1024, else the CTA.
+static int quant_threads(int K) { return K <= 8 * 8 * kQuantVec ? 8 : K <= 32 * 8 * kQuantVec ? 32 : 256; }
+
+// Codes and scales of x [rows, K].
 template <typename T>
 static int launch_quant_rows(const T* x, long long rows, int K, int8_t* q, float* scale, cudaStream_t st) {
-  if (K <= 32 * 8 * kQuantVec)
-    MOE_LAUNCH((k_quant_rows<32, T>), (unsigned)cdiv(rows, 8), 256, 0, st, x, rows, K, q, scale);
-  else
-    MOE_LAUNCH((k_quant_rows<256, T>), (unsigned)rows, 256, 0, st, x, rows, K, q, scale);
+  const int tpr = quant_threads(K);
+  const unsigned blocks = (unsigned)cdiv(rows * tpr, 256);
+  if (tpr == 8) MOE_LAUNCH((k_quant_rows<8, T>), blocks, 256, 0, st, x, rows, K, q, scale);
+  else if (tpr == 32) MOE_LAUNCH((k_quant_rows<32, T>), blocks, 256, 0, st, x, rows, K, q, scale);
+  else MOE_LAUNCH((k_quant_rows<256, T>), blocks, 256, 0, st, x, rows, K, q, scale);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -779,29 +786,102 @@ static int launch_quant_slots(const moe_shape* s, const void* x, const int32_t* 
                               int8_t* q_tok, float* s_tok, cudaStream_t st) {
   const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(x);
   const int R = (int)grouped_rows(s);
-  const bool warp_rows = s->d <= 32 * 8 * kQuantVec;
-  const unsigned blocks = (unsigned)(warp_rows ? cdiv(s->T, 8) : s->T);
+  const int tpr = quant_threads(s->d);
+  const unsigned blocks = (unsigned)cdiv(s->T * (long long)tpr, 256);
+#define MOE_QSLOT_T(T_, N_)                                                                                       \
+  MOE_LAUNCH((k_quant_slots<T_, N_>), blocks, 256, 0, st, xb, slot, (int)s->T, s->d, s->k, R, q, scale, q_tok, s_tok)
 #define MOE_QSLOT(N_)                                                                                             \
   if (s->k <= N_) {                                                                                               \
-    if (warp_rows)                                                                                                \
-      MOE_LAUNCH((k_quant_slots<32, N_>), blocks, 256, 0, st, xb, slot, (int)s->T, s->d, s->k, R, q, scale, q_tok, \
-                 s_tok);                                                                                          \
-    else                                                                                                          \
-      MOE_LAUNCH((k_quant_slots<256, N_>), blocks, 256, 0, st, xb, slot, (int)s->T, s->d, s->k, R, q, scale,       \
-                 q_tok, s_tok);                                                                                   \
+    if (tpr == 8) MOE_QSLOT_T(8, N_);                                                                             \
+    else if (tpr == 32) MOE_QSLOT_T(32, N_);                                                                      \
+    else MOE_QSLOT_T(256, N_);                                                                                    \
     MOE_LAUNCH_CHECK();                                                                                           \
     return MOE_OK;                                                                                                \
   }
   MOE_QSLOT(2) MOE_QSLOT(4) MOE_QSLOT(8) MOE_QSLOT(16)
 #undef MOE_QSLOT
+#undef MOE_QSLOT_T
   return MOE_UNSUPPORTED_SHAPE;
 }
 
-// y = FFN of the codes xq (scales xs) over groups; h [R, hidden] bf16, hq [R, hidden] and hs [R] are scratch.
+// Both products in one kernel (hidden 128 or 256): the codes of h stay in shared memory.
+template <int MODE, int H, int CG>
+static int launch_i8_fused_t(const I8Params& p, const void* xq, const void* w13, const void* w2, const float* s2,
+                             cudaStream_t st) {
+  using Cfg = I8FusedCfg<H, CG>;
+  static std::atomic<unsigned long long> done_mask{0};
+  const unsigned long long bit = 1ull << (current_device() & 63);
+  if (!(done_mask.load(std::memory_order_relaxed) & bit)) {
+    MOE_CUDA_TRY(cudaFuncSetAttribute(k_int8_fused<MODE, H, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)Cfg::kSmemBytes));
+    done_mask.fetch_or(bit);
+  }
+  CUtensorMap tx, txf, t13, t2;
+  const cuuint64_t dx[2] = {(cuuint64_t)p.K, (cuuint64_t)p.R};
+  const cuuint64_t d13[3] = {(cuuint64_t)p.K, (cuuint64_t)(2 * H), (cuuint64_t)p.n_groups};
+  const cuuint64_t d2[3] = {(cuuint64_t)H, (cuuint64_t)p.N, (cuuint64_t)p.n_groups};
+  int rc = make_map_i8(&tx, xq, 2, dx, kBM);
+  if (rc) return rc;
+  rc = make_map_i8(&txf, xq, 2, dx, kI8ABox);
+  if (rc) return rc;
+  rc = make_map_i8(&t13, w13, 3, d13, 128);
+  if (rc) return rc;
+  rc = make_map_i8(&t2, w2, 3, d2, CG == 2 ? 128 : 256);
+  if (rc) return rc;
+  const long long TM = (long long)kBM * CG;
+  const long long tiles = p.group_rows ? (p.R / TM + p.n_groups) : cdiv(p.R, TM);
+  const int units = (int)std::max<long long>(1, std::min<long long>(num_sms() / CG, tiles));
+  MOE_CUDA_TRY(launch_pdl(k_int8_fused<MODE, H, CG>, dim3((unsigned)(CG * units)), dim3(kI8Threads), Cfg::kSmemBytes,
+                          st, (unsigned)CG, tx, txf, t13, t2, p, s2));
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+static int launch_i8_fused(const moe_shape* s, int hidden, const I8Params& p, const void* xq, const void* w13,
+                           const void* w2, const float* s2, cudaStream_t st) {
+  const bool pair = !(s->flags & MOE_FLAG_SINGLE_CTA_GEMM) && p.R >= 192ll * p.n_groups;
+  const bool geglu = s->act == MOE_ACT_GEGLU;
+#define MOE_I8_FUSED(M_, H_, CG_) \
+  if ((M_ == kModeGeGLU) == geglu && hidden == H_ && (CG_ == 2) == pair) \
+    return launch_i8_fused_t<M_, H_, CG_>(p, xq, w13, w2, s2, st);
+  MOE_I8_FUSED(kModeSwiGLU, 256, 2) MOE_I8_FUSED(kModeSwiGLU, 256, 1) MOE_I8_FUSED(kModeSwiGLU, 128, 2)
+  MOE_I8_FUSED(kModeSwiGLU, 128, 1) MOE_I8_FUSED(kModeGeGLU, 256, 2) MOE_I8_FUSED(kModeGeGLU, 256, 1)
+  MOE_I8_FUSED(kModeGeGLU, 128, 2) MOE_I8_FUSED(kModeGeGLU, 128, 1)
+#undef MOE_I8_FUSED
+  return MOE_UNSUPPORTED_SHAPE;
+}
+
+// One kernel for both products, or the products with h in memory between them.  The fused kernel gives a row tile to
+// one CTA (pair), which streams its expert's weights alone: right where the row tiles fill the GPU, and where an
+// expert is small enough that one SM streams it in the time that two more launches take.
+static bool use_i8_fused(const moe_shape* s, int hidden, long long R, int n_groups) {
+  if (hidden != 128 && hidden != 256) return false;
+  const long long expert_bytes = 3ll * s->d * hidden;
+  return expert_bytes <= (3ll << 19) || R >= 64ll * num_sms();
+}
+
+// y = FFN of the codes xq (scales xs) over groups; h [R, hidden] bf16, hq [R, hidden] and hs [R] are scratch, not
+// touched by the fused kernel.
 static int int8_ffn(const moe_shape* s, int hidden, long long R, const void* xq, const float* xs,
                     const int32_t* gstart, const int32_t* grows, int n_groups, const void* w13, const float* s13,
                     const void* w2, const float* s2, void* h, void* hq, float* hs, void* y, cudaStream_t st) {
   if (R == 0) return MOE_OK;
+  if (use_i8_fused(s, hidden, R, n_groups)) {
+    I8Params p{};
+    p.group_start = gstart;
+    p.group_rows = grows;
+    p.n_groups = n_groups;
+    p.R = R;
+    p.K = s->d;
+    p.N = s->d;
+    p.up_row0 = hidden;
+    p.b_rows = 2 * hidden;
+    p.a_scale = xs;
+    p.b_scale = s13;
+    p.out = reinterpret_cast<__nv_bfloat16*>(y);
+    p.wait_limit_ns = g_wait_limit_ns.load();
+    return launch_i8_fused(s, hidden, p, xq, w13, w2, s2, st);
+  }
   const bool pair = !(s->flags & MOE_FLAG_SINGLE_CTA_GEMM);
   int rc = int8_gemm(s->act == MOE_ACT_SWIGLU ? kModeSwiGLU : kModeGeGLU, xq, xs, R, s->d, w13, s13, n_groups,
                      2 * hidden, hidden, hidden, gstart, grows, h, st, pair);
@@ -818,11 +898,12 @@ static int int8_ffn(const moe_shape* s, int hidden, long long R, const void* xq,
     p.n_groups = n_groups;
     p.R = R;
     p.K = hidden;
+    const int tpr = quant_threads(hidden);
     const long long most = 8ll * num_sms();   // 256-thread CTAs resident at once
-    if (hidden <= 32 * 8 * kQuantVec)
-      MOE_LAUNCH((k_quant_groups<32>), (unsigned)std::min(most, cdiv(R, 8)), 256, 0, st, hb, p, hc, hs);
-    else
-      MOE_LAUNCH((k_quant_groups<256>), (unsigned)std::min(most, R), 256, 0, st, hb, p, hc, hs);
+    const unsigned blocks = (unsigned)std::min(most, cdiv(R * tpr, 256));
+    if (tpr == 8) MOE_LAUNCH((k_quant_groups<8>), blocks, 256, 0, st, hb, p, hc, hs);
+    else if (tpr == 32) MOE_LAUNCH((k_quant_groups<32>), blocks, 256, 0, st, hb, p, hc, hs);
+    else MOE_LAUNCH((k_quant_groups<256>), blocks, 256, 0, st, hb, p, hc, hs);
     MOE_LAUNCH_CHECK();
   }
   return int8_gemm(kModePlain, hq, hs, R, hidden, w2, s2, n_groups, s->d, 0, s->d, gstart, grows, y, st, pair);

@@ -242,6 +242,23 @@ def test_bf16_entry_quantises_and_runs_the_same(lib):
                                    group_rows=t([0, 0, 0])).shape == (0, 256)
 
 
+def test_outputs_and_inputs_on_16_byte_boundaries(lib):
+    moe = lib
+    s, x, dv, starts, rows, y = _ffn_case(moe, 208, 64, 0, [33, 0, 200])
+    t = lambda v: torch.from_numpy(np.asarray(v).astype(np.int32)).to(DEV)  # noqa: E731
+
+    def shifted(a, n):   # the same values n elements behind a 256-byte boundary
+        b = torch.empty(a.numel() + n, dtype=a.dtype, device=DEV)
+        b[n:] = a.reshape(-1)
+        return b[n:].view(a.shape)
+    xq, xs = moe.moe_quantize_int8(shifted(x.to(DEV), 8))
+    out = shifted(torch.zeros_like(y), 8)
+    w = {k_: shifted(v, 16 // v.element_size()) for k_, v in dv.items()}
+    got = moe.moe_expert_ffn_int8(s, shifted(xq, 16), shifted(xs, 4), w["w13"], w["s13"], w["w2"], w["s2"],
+                                  group_start=t(starts), group_rows=t(rows), y=out)
+    assert got.data_ptr() % 32 == 16 and torch.equal(got, y)
+
+
 # ---------------------------------------------------------------- the layer
 
 
