@@ -10,11 +10,15 @@
 // threads that share a row through shared memory, and the codes (128 bytes a row per 128 columns) are the A operand
 // of the down product as they lie.
 //
-// Order of work of one CTA (pair): gate/up of tile i + 1 before down of tile i.  The tensor core then has a tile's
-// gate/up to do while the epilogue turns the tile before it into codes; h is double-buffered.  Jobs alternate between
-// two TMEM accumulators of 256 columns, so an epilogue overlaps the next job's MMAs.  h of tile i is rewritten by the
-// epilogue of tile i + 2's gate/up, whose accumulator is ready only after every MMA issued before it, down of tile i
-// among them.  Roles as k_int8_gemm: warp 0 TMA, warp 1 MMA, warps 4-19 epilogue.
+// Order of work of one CTA (pair): the gate/up jobs of tile i + 1 spread between the down jobs of tile i, then the
+// codes of tile i + 1 (for d = 768, H = 256: G0 D0 G1 D1 D2 C).  The tensor core has the next tile's first gate/up job
+// to do while the epilogue makes the codes, and a gate/up job's long MMA loop runs beside the stores of a down job.
+// Jobs alternate between two TMEM accumulators of 256 columns, so an epilogue overlaps the next job's MMAs.  The codes
+// of tile i + 1 replace those of tile i after the epilogue has seen tile i's last down accumulator, that is after every
+// MMA that reads them.  The epilogue is what the kernel waits for, so it is kept lean: channel scales come by bulk
+// copies of the producer, y leaves through shared memory by TMA (a warp's 32 rows x 64 columns at a time; stores from
+// registers touch 32 lines each and held up the fence before the codes are published), and warps without rows skip
+// the arithmetic.  Roles as k_int8_gemm: warp 0 TMA, warp 1 MMA, warps 4-19 epilogue.
 #pragma once
 
 #include "int8_gemm.cuh"
@@ -23,14 +27,15 @@ namespace moe {
 
 template <int H, int CG>
 struct I8FusedCfg {
-  static constexpr int kHBytes = (H / 128) * kBM * 128;              // one buffer of h codes: 16 KB per 128 columns
+  static constexpr int kHBytes = (H / 128) * kBM * 128;              // h codes: 16 KB per 128 columns
   static constexpr int kABytes = kBM * kI8BK;
   static constexpr int kBBytes = (CG == 2 ? 128 : 256) * kI8BK;      // a 256-row B box, half of it per CTA of a pair
   static constexpr int kSlotBytes = kABytes + kBBytes;
   static constexpr int kDownSteps = CG == 2 ? H / 128 : 1;           // down k-steps whose B boxes share a slot
-  static constexpr int kBudget = 212 * 1024 - 1024 - 2 * kHBytes;
+  static constexpr int kOutBytes = CG == 2 ? kI8EpiWarps * 32 * 128 : 0;   // y staging: 4 KB per epilogue warp
+  static constexpr int kBudget = 208 * 1024 - 1024 - kHBytes - kOutBytes;
   static constexpr int kStages = kBudget / kSlotBytes > 8 ? 8 : kBudget / kSlotBytes;
-  static constexpr size_t kSmemBytes = 1024 + 2 * (size_t)kHBytes + (size_t)kStages * kSlotBytes;
+  static constexpr size_t kSmemBytes = 1024 + (size_t)kHBytes + kOutBytes + (size_t)kStages * kSlotBytes;
   static_assert(kStages >= 2 && kDownSteps * kBBytes <= kSlotBytes, "shared memory budget");
 };
 
@@ -38,8 +43,8 @@ struct I8FusedCfg {
 template <int MODE, int H, int CG>
 __global__ void __launch_bounds__(kI8Threads, 1)
     k_int8_fused(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXFew,
-                 const __grid_constant__ CUtensorMap tmW13, const __grid_constant__ CUtensorMap tmW2, const I8Params p,
-                 const float* __restrict__ s2) {
+                 const __grid_constant__ CUtensorMap tmW13, const __grid_constant__ CUtensorMap tmW2,
+                 const __grid_constant__ CUtensorMap tmY, const I8Params p, const float* __restrict__ s2) {
   pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
   using Cfg = I8FusedCfg<H, CG>;
   static_assert(H == 128 || H == 256, "fused expert hidden width");
@@ -52,14 +57,18 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* ring = smem + 2 * Cfg::kHBytes;          // h codes: [2][128 columns][128 rows][128 B], swizzled
-  __shared__ __align__(8) uint64_t bar_full[S], bar_empty[S], bar_tfull[2], bar_tempty[2], bar_hready[2], bar_final;
+  // h codes [128 columns][128 rows][128 B], y staging [16 warps][32 rows][128 B] (both swizzled), ring
+  uint8_t* stage_y = smem + Cfg::kHBytes;
+  uint8_t* ring = stage_y + Cfg::kOutBytes;
+  __shared__ __align__(8) uint64_t bar_full[S], bar_empty[S], bar_tfull[2], bar_tempty[2], bar_hready, bar_final;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_prefix[kMaxGroupsSmem + 1];
   __shared__ int s_gstart[kMaxGroupsSmem];
   __shared__ int s_grows[kMaxGroupsSmem];
-  __shared__ __align__(16) float s_scale[kI8EpiWarps][64];
+  // channel scales of the jobs in flight (gate then up, or 256 of s2), copied in by the producer
+  __shared__ __align__(16) float s_scale[kI8ScaleBufs][256];
+  __shared__ __align__(8) uint64_t bar_sfull[kI8ScaleBufs], bar_sempty[kI8ScaleBufs];
   __shared__ uint32_t s_top[2][4][kBM];             // partial row maxima of h, by tile parity
 
   const int warp = warp_id(), lane = lane_id();
@@ -76,8 +85,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     for (int a = 0; a < 2; ++a) {
       mbar_init(&bar_tfull[a], 1);
       mbar_init(&bar_tempty[a], CG * kI8EpiWarps);
-      mbar_init(&bar_hready[a], CG * kI8EpiWarps);
     }
+    mbar_init(&bar_hready, CG * kI8EpiWarps);
+    for (int b = 0; b < kI8ScaleBufs; ++b) { mbar_init(&bar_sfull[b], 1); mbar_init(&bar_sempty[b], kI8EpiWarps); }
     mbar_init(&bar_final, 1);
     s_abort = 0;
     fence_mbar_init();
@@ -85,6 +95,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     tma_prefetch_desc(&tmXFew);
     tma_prefetch_desc(&tmW13);
     tma_prefetch_desc(&tmW2);
+    if (Cfg::kOutBytes > 0) tma_prefetch_desc(&tmY);
   }
   if (warp == 1) {
     if (kPair) {
@@ -116,7 +127,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      long long issued = 0;
+      long long issued = 0, scales = 0;
       auto loaded = [](int rows) {
         return rows <= 0 ? 0 : rows > kI8Few ? kBM : (rows + kI8ABox - 1) / kI8ABox * kI8ABox;
       };
@@ -134,21 +145,36 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         if (kPair) tma_load_3d_pair(dst, map, mapa_shared(smem_u32(&bar_full[stage]), 0), k0, row, g);
         else tma_load_3d(dst, map, &bar_full[stage], k0, row, g);
       };
+      // a job's channel scales: n floats of a (and of b, behind 128 floats)
+      auto load_scales = [&](const float* a, const float* b, int n) {
+        const int k = (int)(scales % kI8ScaleBufs);
+        if (!mbar_wait(&bar_sempty[k], (uint32_t)((scales / kI8ScaleBufs) & 1) ^ 1u, p.wait_limit_ns, &s_abort, 0x0609))
+          return false;
+        mbar_arrive_expect_tx(&bar_sfull[k], (uint32_t)n * (b != nullptr ? 8u : 4u));
+        bulk_load(&s_scale[k][0], a, (uint32_t)n * 4, &bar_sfull[k]);
+        if (b != nullptr) bulk_load(&s_scale[k][128], b, (uint32_t)n * 4, &bar_sfull[k]);
+        ++scales;
+        return true;
+      };
       bool ok = true;
       for (int i = 0; i <= mine && ok && !s_abort; ++i) {
-        int g, row0, rows_left;
-        if (i < mine) {
-          locate(i, g, row0, rows_left);
-          const int na = loaded(rows_left - crank * kBM);
-          const int na_all = kPair ? loaded(rows_left) + loaded(rows_left - kBM) : na;
-          const uint32_t bytes = (uint32_t)(na_all * kI8BK + CG * Cfg::kBBytes);
+        int g = 0, row0 = 0, rows_left = 0, gd = 0, rd, ld;
+        if (i < mine) locate(i, g, row0, rows_left);
+        if (i > 0) locate(i - 1, gd, rd, ld);
+        const int na = loaded(rows_left - crank * kBM);
+        const int na_all = kPair ? loaded(rows_left) + loaded(rows_left - kBM) : na;
+        const uint32_t bytes = (uint32_t)(na_all * kI8BK + CG * Cfg::kBBytes);
+        const CUtensorMap* mx = na == kBM ? &tmX : &tmXFew;
+        const int step = na == kBM ? kBM : kI8ABox;
+        for (int jd = 0; jd < nd && ok; ++jd) {
           for (int job = 0; job < NGU && ok; ++job) {
-            for (int kb = 0; kb < nk; ++kb) {
+            if (i == mine || job * nd / NGU != jd) continue;
+            const float* s13 = p.b_scale + (size_t)g * (2 * H) + 128 * job;
+            ok = load_scales(s13, s13 + H, 128);
+            for (int kb = 0; ok && kb < nk; ++kb) {
               if (!(ok = arm(bytes))) break;
               uint8_t* a_s = ring + (size_t)stage * Cfg::kSlotBytes;
               uint8_t* b_s = a_s + Cfg::kABytes;
-              const CUtensorMap* mx = na == kBM ? &tmX : &tmXFew;
-              const int step = na == kBM ? kBM : kI8ABox;
               for (int r = 0; r < na; r += step) {
                 if (kPair)
                   tma_load_2d_pair(a_s + r * kI8BK, mx, mapa_shared(smem_u32(&bar_full[stage]), 0), kb * kI8BK,
@@ -165,17 +191,13 @@ __global__ void __launch_bounds__(kI8Threads, 1)
               next();
             }
           }
-        }
-        if (i > 0 && ok) {
-          locate(i - 1, g, row0, rows_left);
-          for (int job = 0; job < nd && ok; ++job) {
-            for (int kb = 0; kb < NKD; kb += Cfg::kDownSteps) {
-              if (!(ok = arm((uint32_t)(CG * Cfg::kDownSteps * Cfg::kBBytes)))) break;
-              uint8_t* b_s = ring + (size_t)stage * Cfg::kSlotBytes;
-              for (int j = 0; j < Cfg::kDownSteps; ++j)
-                load_b(b_s + j * Cfg::kBBytes, &tmW2, (kb + j) * kI8BK, 256 * job + 128 * crank, g);
-              next();
-            }
+          if (i > 0 && ok) ok = load_scales(s2 + (size_t)gd * p.N + 256 * jd, nullptr, min(256, p.N - 256 * jd));
+          for (int kb = 0; i > 0 && ok && kb < NKD; kb += Cfg::kDownSteps) {
+            if (!(ok = arm((uint32_t)(CG * Cfg::kDownSteps * Cfg::kBBytes)))) break;
+            uint8_t* b_s = ring + (size_t)stage * Cfg::kSlotBytes;
+            for (int j = 0; j < Cfg::kDownSteps; ++j)
+              load_b(b_s + j * Cfg::kBBytes, &tmW2, (kb + j) * kI8BK, 256 * jd + 128 * crank, gd);
+            next();
           }
         }
       }
@@ -188,6 +210,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           mbar_wait(&bar_full[(int)(n % S)], (uint32_t)((n / S) & 1), p.wait_limit_ns, &dummy, 0x0602);
         }
       }
+      i8_drain_scales(bar_sfull, scales, p.wait_limit_ns, 0x060A);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -224,8 +247,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       };
       bool ok = true;
       for (int i = 0; i <= mine && ok && !s_abort; ++i) {
-        if (i < mine) {
+        const int t = i - 1;
+        for (int jd = 0; jd < nd && ok; ++jd) {
           for (int job = 0; job < NGU && ok; ++job) {
+            if (i == mine || job * nd / NGU != jd) continue;
             if (!(ok = acquire())) break;
             const uint32_t d_tmem = tmem_base + (uint32_t)(slot * 256);
             for (int kb = 0; kb < nk; ++kb) {
@@ -236,27 +261,24 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             }
             if (ok) publish();
           }
-        }
-        if (i > 0 && ok) {
-          const int t = i - 1;
-          // h codes of tile t, written by both CTAs' epilogues
-          if (!(ok = mbar_wait_cluster(&bar_hready[t & 1], (uint32_t)((t >> 1) & 1), p.wait_limit_ns, &s_abort, 0x0604)))
-            break;
-          tc_fence_after();
-          for (int job = 0; job < nd && ok; ++job) {
-            if (!(ok = acquire())) break;
-            const uint32_t d_tmem = tmem_base + (uint32_t)(slot * 256);
-            for (int kb = 0; kb < NKD; kb += Cfg::kDownSteps) {
-              if (!(ok = full())) break;
-              const uint32_t b_addr = smem_u32(ring + (size_t)stage * Cfg::kSlotBytes);
-#pragma unroll
-              for (int j = 0; j < Cfg::kDownSteps; ++j)
-                mma128(d_tmem, h_addr + (uint32_t)((t & 1) * Cfg::kHBytes + (kb + j) * (kBM * 128)),
-                       b_addr + (uint32_t)(j * Cfg::kBBytes), kb + j == 0);
-              release_stage();
-            }
-            if (ok) publish();
+          if (i == 0 || !ok) continue;
+          if (jd == 0) {   // h codes of tile t, written by both CTAs' epilogues
+            ok = mbar_wait_cluster(&bar_hready, (uint32_t)(t & 1), p.wait_limit_ns, &s_abort, 0x0604);
+            if (!ok) break;
+            tc_fence_after();
           }
+          if (!(ok = acquire())) break;
+          const uint32_t d_tmem = tmem_base + (uint32_t)(slot * 256);
+          for (int kb = 0; kb < NKD; kb += Cfg::kDownSteps) {
+            if (!(ok = full())) break;
+            const uint32_t b_addr = smem_u32(ring + (size_t)stage * Cfg::kSlotBytes);
+#pragma unroll
+            for (int j = 0; j < Cfg::kDownSteps; ++j)
+              mma128(d_tmem, h_addr + (uint32_t)((kb + j) * (kBM * 128)),
+                     b_addr + (uint32_t)(j * Cfg::kBBytes), kb + j == 0);
+            release_stage();
+          }
+          if (ok) publish();
         }
       }
       if (kPair) tc_commit_pair(&bar_final);
@@ -272,10 +294,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     const int part = ew >> 2;                // this warp's quarter of a job's columns
     const int row = q * 32 + lane;           // this thread's row of the tile
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-    float* scl = s_scale[ew];
     int slot = 0;
     uint32_t slot_phase = 0;
-    float hs = 0.f, hs_prev = 0.f;           // scale of this row's codes: the tile just encoded, the one before
+    long long n_job = 0;
+    float hs = 0.f;                          // scale of this row's codes in the tile encoded last
     auto arrive = [&](uint64_t* bar) {       // one arrival per warp, on the leader's barrier
       __syncwarp();
       if (lane == 0) {
@@ -284,65 +306,153 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       }
     };
     bool ok = true;
-    // after a wait that gave up the loop runs on without waits or stores, so that all 16 warps meet at the barrier
+    // the job's channel scales and accumulator
+    auto job_ready = [&]() {
+      const int k = (int)(n_job % kI8ScaleBufs);
+      if (!mbar_wait(&bar_sfull[k], (uint32_t)((n_job / kI8ScaleBufs) & 1), p.wait_limit_ns, &s_abort, 0x060B)) return false;
+      if (!mbar_wait(&bar_tfull[slot], slot_phase, p.wait_limit_ns, &s_abort, 0x0607)) return false;
+      tc_fence_after();
+      return true;
+    };
+    auto job_done = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_sempty[(int)(n_job % kI8ScaleBufs)]);
+      ++n_job;
+      if (++slot == 2) { slot = 0; slot_phase ^= 1u; }
+    };
+    // tile i's rows and this thread's token scale are fetched a tile ahead
+    int g_n, row0_n = 0, left_n = 0, row0 = 0;
+    float sx_n = 0.f;
+    auto fetch = [&](int i) {
+      left_n = 0;
+      sx_n = 0.f;
+      if (i >= mine) return;
+      locate(i, g_n, row0_n, left_n);
+      if (row < left_n - crank * kBM) sx_n = p.a_scale[(long long)row0_n + row];
+    };
+    fetch(0);
+    uint8_t* my_y = stage_y + ew * (32 * 128);
+    uint8_t* h_row = smem + (size_t)row * 128;
+    const uint32_t sw = (uint32_t)(row & 7);
+    int nv = 0;                              // rows of this warp in tile i
     for (int i = 0; i <= mine; ++i) {
-      int g, row0, rows_left;
-      if (i < mine) {
-        locate(i, g, row0, rows_left);
-        const bool live = row < rows_left - crank * kBM;
-        const float sx = live ? p.a_scale[(long long)row0 + row] : 0.f;
-        const float* s13 = p.b_scale + (size_t)g * (2 * H) + 32 * part + lane;
-        uint32_t hv[NGU][16] = {};           // h, bf16 pairs: 32 columns per job
-        uint32_t top = 0;                    // maximum of |h| as bf16 bits, per half word
+      const int nv_d = nv;                   // and in tile i - 1
+      const long long y_row0 = (long long)row0 + q * 32;
+      const float hs_d = hs;                 // scale of this row's codes in tile i - 1
+      row0 = row0_n;
+      nv = max(0, min(32, left_n - crank * kBM - q * 32));
+      const float sx = sx_n;
+      fetch(i + 1);
+      uint32_t hv[NGU][16];                  // h of tile i, bf16 pairs: 32 columns per job
+      uint32_t top = 0;                      // maximum of |h| as bf16 bits, per half word
+      for (int jd = 0; jd < nd; ++jd) {
 #pragma unroll
         for (int job = 0; job < NGU; ++job) {
-          if (!ok) break;
-          __syncwarp();
-          scl[lane] = s13[128 * job];
-          scl[32 + lane] = s13[H + 128 * job];
-          __syncwarp();
-          if (!mbar_wait(&bar_tfull[slot], slot_phase, p.wait_limit_ns, &s_abort, 0x0607)) { ok = false; break; }
-          tc_fence_after();
+          if (i == mine || job * nd / NGU != jd || !ok || !(ok = job_ready())) continue;
+          const float* scl = &s_scale[(int)(n_job % kI8ScaleBufs)][32 * part];
           const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(slot * 256 + 32 * part);
+          if (nv == 0) {
+            arrive(&bar_tempty[slot]);
+            job_done();
+            continue;
+          }
+          uint32_t v[2][16], u[2][16];
+          tmem_ld16(t_row, v[0]);
+          tmem_ld16(t_row + 128, u[0]);
 #pragma unroll
           for (int c0 = 0; c0 < 32; c0 += 16) {
-            uint32_t v[16], u[16];
-            tmem_ld16(t_row + c0, v);
-            tmem_ld16(t_row + 128 + c0, u);
             tmem_ld_wait();
-            if (c0 == 16) {
+            if (c0 == 0) {
+              tmem_ld16(t_row + 16, v[1]);
+              tmem_ld16(t_row + 144, u[1]);
+            } else {
               tc_fence_before();
               arrive(&bar_tempty[slot]);
             }
+            const uint32_t* vc = v[c0 / 16];
+            const uint32_t* uc = u[c0 / 16];
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
               const float4 sg = *reinterpret_cast<const float4*>(scl + c0 + j);
-              const float4 su = *reinterpret_cast<const float4*>(scl + 32 + c0 + j);
-              const float gs[4] = {sg.x, sg.y, sg.z, sg.w}, us[4] = {su.x, su.y, su.z, su.w};
-              float f[4];
-#pragma unroll
-              for (int l = 0; l < 4; ++l)
-                f[l] = i8_act<MODE>((float)(int)v[j + l] * sx * gs[l]) * ((float)(int)u[j + l] * sx * us[l]);
-              hv[job][(c0 + j) / 2] = pack_bf16x2(f[0], f[1]);
-              hv[job][(c0 + j) / 2 + 1] = pack_bf16x2(f[2], f[3]);
-              top = __vmaxu2(top, __vmaxu2(hv[job][(c0 + j) / 2] & 0x7FFF7FFFu,
-                                           hv[job][(c0 + j) / 2 + 1] & 0x7FFF7FFFu));
+              const float4 su = *reinterpret_cast<const float4*>(scl + 128 + c0 + j);
+              const float2 f0 = i8_glu2<MODE>(i8_scaled(vc[j], vc[j + 1], sx, sg.x, sg.y),
+                                              i8_scaled(uc[j], uc[j + 1], sx, su.x, su.y));
+              const float2 f1 = i8_glu2<MODE>(i8_scaled(vc[j + 2], vc[j + 3], sx, sg.z, sg.w),
+                                              i8_scaled(uc[j + 2], uc[j + 3], sx, su.z, su.w));
+              const uint32_t p0 = pack_bf16x2(f0.x, f0.y), p1 = pack_bf16x2(f1.x, f1.y);
+              hv[job][(c0 + j) / 2] = p0;
+              hv[job][(c0 + j) / 2 + 1] = p1;
+              top = __vmaxu2(top, __vmaxu2(p0 & 0x7FFF7FFFu, p1 & 0x7FFF7FFFu));
             }
           }
-          if (++slot == 2) { slot = 0; slot_phase ^= 1u; }
+          job_done();
         }
-        // the row's maximum over its four threads, then the codes into the operand layout: the row's 128 bytes of a
-        // 128-column atom, 16-byte chunk c at position c ^ (row & 7)
-        s_top[i & 1][part][row] = max(top << 16, top & 0xFFFF0000u);
-        named_bar_sync(1, kI8EpiWarps * 32);
+        if (i == 0 || !ok || !(ok = job_ready())) continue;
+        const int cols = p.N - 256 * jd - 64 * part;   // a multiple of 16, may be <= 0
+        const float* scl = &s_scale[(int)(n_job % kI8ScaleBufs)][64 * part];
+        const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(slot * 256 + 64 * part);
+        if (nv_d == 0 || cols <= 0) {
+          arrive(&bar_tempty[slot]);
+          job_done();
+          continue;
+        }
+        const bool by_tma = kPair && nv_d == 32;       // a warp whose rows all belong to the group
+        if (by_tma) {
+          if (lane == 0) bulk_wait_read();             // the last store has left the staging rows
+          __syncwarp();
+        }
+        uint32_t v[2][16];
+        tmem_ld16(t_row, v[0]);
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 16) {
+          const uint32_t* vc = v[(c0 / 16) & 1];
+          tmem_ld_wait();
+          if (c0 < 48) {
+            tmem_ld16(t_row + c0 + 16, v[((c0 / 16) & 1) ^ 1]);
+          } else {
+            tc_fence_before();
+            arrive(&bar_tempty[slot]);
+          }
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 sg = *reinterpret_cast<const float4*>(scl + c0 + j);
+            const float2 f0 = i8_scaled(vc[j], vc[j + 1], hs_d, sg.x, sg.y);
+            const float2 f1 = i8_scaled(vc[j + 2], vc[j + 3], hs_d, sg.z, sg.w);
+            o[j / 2] = pack_bf16x2(f0.x, f0.y);
+            o[j / 2 + 1] = pack_bf16x2(f1.x, f1.y);
+          }
+          if (by_tma) {   // staging row = lane, 16-byte chunk c at c ^ (lane & 7)
+            uint4* r = reinterpret_cast<uint4*>(my_y + lane * 128);
+            r[(uint32_t)(c0 / 8) ^ (uint32_t)(lane & 7)] = make_uint4(o[0], o[1], o[2], o[3]);
+            r[(uint32_t)(c0 / 8 + 1) ^ (uint32_t)(lane & 7)] = make_uint4(o[4], o[5], o[6], o[7]);
+          } else if (lane < nv_d && c0 < cols) {
+            st_row16(p.out + (y_row0 + lane) * p.N + 256 * jd + 64 * part + c0, o, wide);
+          }
+        }
+        if (by_tma) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmY, my_y, 256 * jd + 64 * part, (int)y_row0);
+            bulk_commit();
+          }
+        }
+        job_done();
+      }
+      if (i == mine) break;
+      // codes of tile i: the row's maximum over its four threads, then the row's 128 bytes of a 128-column atom of the
+      // operand layout, 16-byte chunk c at position c ^ (row & 7).  Every warp comes here, also after a wait that gave
+      // up (it then waits for and stores nothing any more), so that the barrier is whole.
+      s_top[i & 1][part][row] = max(top << 16, top & 0xFFFF0000u);
+      named_bar_sync(1, kI8EpiWarps * 32);
+      if (!ok) continue;
+      if (nv > 0) {
         uint32_t m = s_top[i & 1][0][row];
 #pragma unroll
         for (int k = 1; k < 4; ++k) m = max(m, s_top[i & 1][k][row]);
         float r;
-        hs_prev = hs;
         quant_scale(__uint_as_float(m), hs, r);
-        uint8_t* h_row = smem + (size_t)(i & 1) * Cfg::kHBytes + (size_t)row * 128;
-        const uint32_t sw = (uint32_t)(row & 7);
 #pragma unroll
         for (int job = 0; job < NGU; ++job) {
 #pragma unroll
@@ -358,52 +468,15 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
-        // publish to the tensor core (async proxy) and to the leader's MMA issuer
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (kPair) mbar_arrive_cluster_release(mapa_shared(smem_u32(&bar_hready[i & 1]), 0));
-          else mbar_arrive(&bar_hready[i & 1]);
-        }
-      } else {
-        hs_prev = hs;
+        fence_proxy_async_smem();   // the tensor core reads them through the async proxy
       }
-      if (i > 0 && ok) {
-        locate(i - 1, g, row0, rows_left);
-        const bool live = row < rows_left - crank * kBM;
-        __nv_bfloat16* out = p.out + ((long long)row0 + row) * p.N + 64 * part;
-        const float* s2g = s2 + (size_t)g * p.N + 64 * part;
-        for (int job = 0; job < nd; ++job) {
-          const int cols = p.N - 256 * job - 64 * part;   // a multiple of 16, may be <= 0
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 64; c += 32) scl[c + lane] = c + lane < cols ? s2g[256 * job + c + lane] : 0.f;
-          __syncwarp();
-          if (!mbar_wait(&bar_tfull[slot], slot_phase, p.wait_limit_ns, &s_abort, 0x0608)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(slot * 256 + 64 * part);
-#pragma unroll
-          for (int c0 = 0; c0 < 64; c0 += 16) {
-            uint32_t v[16];
-            tmem_ld16(t_row + c0, v);
-            tmem_ld_wait();
-            if (c0 == 48) {
-              tc_fence_before();
-              arrive(&bar_tempty[slot]);
-            }
-            uint32_t o[8];
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 sg = *reinterpret_cast<const float4*>(scl + c0 + j);
-              o[j / 2] = pack_bf16x2((float)(int)v[j] * hs_prev * sg.x, (float)(int)v[j + 1] * hs_prev * sg.y);
-              o[j / 2 + 1] = pack_bf16x2((float)(int)v[j + 2] * hs_prev * sg.z, (float)(int)v[j + 3] * hs_prev * sg.w);
-            }
-            if (live && c0 < cols) st_row16(out + 256 * job + c0, o, wide);
-          }
-          if (++slot == 2) { slot = 0; slot_phase ^= 1u; }
-        }
+      __syncwarp();
+      if (lane == 0) {
+        if (kPair) mbar_arrive_cluster_release(mapa_shared(smem_u32(&bar_hready), 0));
+        else mbar_arrive(&bar_hready);
       }
     }
+    if (kPair && lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   if (kPair) cluster_sync_all();

@@ -45,6 +45,7 @@ constexpr int kI8BK = 128;                      // codes per k-step: one 128-byt
 constexpr int kI8ABox = 32;                     // rows per A box of a tile of at most kI8Few rows, else kBM
 constexpr int kI8Few = 64;
 constexpr int kI8EpiWarps = 16;
+constexpr int kI8ScaleBufs = 8;                 // tiles (or jobs) whose channel scales are in flight
 constexpr int kI8Threads = (4 + kI8EpiWarps) * 32;
 
 template <int BN, int CG>
@@ -52,7 +53,7 @@ struct I8Cfg {
   static constexpr int kABytes = kBM * kI8BK;
   static constexpr int kBBytes = (CG == 2 ? BN / 2 : BN) * kI8BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kBudget = 215 * 1024 - 1024;
+  static constexpr int kBudget = 211 * 1024 - 1024;
   static constexpr int kStages = kBudget / kStageBytes > 8 ? 8 : kBudget / kStageBytes;
   static constexpr int kTmemCols = 2 * BN;      // two accumulators (128, 256 or 512 columns)
   static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes;
@@ -109,19 +110,42 @@ __device__ __forceinline__ float ex2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// act(g) with few instructions.  SiLU: g / (1 + exp(-g)).  GELU: g Phi(g) = max(g, 0) - |g| Q(|g|) with the normal
-// tail Q(a) = erfc(a / sqrt 2) / 2 by Abramowitz & Stegun 7.1.26 (the factor 1/2 and the sqrt 2 folded into its
-// coefficients); the tail form does not cancel for negative g.
+// Two columns of an accumulator, scaled: float(sum) * s_row * s_col.
+__device__ __forceinline__ float2 i8_scaled(uint32_t v0, uint32_t v1, float row, float c0, float c1) {
+  const float2 f = make_float2((float)(int)v0, (float)(int)v1);
+  return __fmul2_rn(__fmul2_rn(f, make_float2(row, row)), make_float2(c0, c1));
+}
+
+// act(g) u of two columns, in packed fp32 pairs.  SiLU: g / (1 + exp(-g)).  GELU: g Phi(g) = max(g, 0) - |g| Q(|g|)
+// with the normal tail Q(a) = erfc(a / sqrt 2) / 2 by Abramowitz & Stegun 7.1.26 (the factor 1/2 and the sqrt 2
+// folded into its coefficients); the tail form does not cancel for negative g.
 template <int MODE>
-__device__ __forceinline__ float i8_act(float g) {
-  if (MODE == kModeSwiGLU) return g * rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * g));
-  const float a = fabsf(g);
-  const float t = rcp_approx(fmaf(0.3275911f * 0.7071067811865476f, a, 1.0f));
-  const float poly = t * (0.5f * 0.254829592f +
-                          t * (-0.5f * 0.284496736f +
-                               t * (0.5f * 1.421413741f + t * (-0.5f * 1.453152027f + t * (0.5f * 1.061405429f)))));
-  const float e = ex2_approx(-0.7213475204444817f * (g * g));
-  return fmaf(-a, poly * e, fmaxf(g, 0.0f));
+__device__ __forceinline__ float2 i8_glu2(float2 g, float2 u) {
+  auto both = [](float c) { return make_float2(c, c); };
+  if (MODE == kModeSwiGLU) {
+    const float2 x = __fmul2_rn(g, both(-1.4426950408889634f));
+    const float2 d = __fadd2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), both(1.0f));
+    return __fmul2_rn(__fmul2_rn(g, make_float2(rcp_approx(d.x), rcp_approx(d.y))), u);
+  }
+  const float2 a = make_float2(fabsf(g.x), fabsf(g.y));
+  const float2 d = __ffma2_rn(both(0.3275911f * 0.7071067811865476f), a, both(1.0f));
+  const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  float2 poly = __ffma2_rn(t, both(0.5f * 1.061405429f), both(-0.5f * 1.453152027f));
+  poly = __ffma2_rn(t, poly, both(0.5f * 1.421413741f));
+  poly = __ffma2_rn(t, poly, both(-0.5f * 0.284496736f));
+  poly = __ffma2_rn(t, poly, both(0.5f * 0.254829592f));
+  const float2 x = __fmul2_rn(__fmul2_rn(g, g), both(-0.7213475204444817f));
+  const float2 q = __fmul2_rn(__fmul2_rn(t, poly), make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+  return __fmul2_rn(__ffma2_rn(make_float2(-a.x, -a.y), q, make_float2(fmaxf(g.x, 0.f), fmaxf(g.y, 0.f))), u);
+}
+
+// Wait for the scale copies still in flight (the last kI8ScaleBufs of n): none may land after the CTA has ended.
+__device__ __forceinline__ void i8_drain_scales(uint64_t* bar_sfull, long long n, uint64_t limit_ns, unsigned int site) {
+  for (int i = 1; i <= kI8ScaleBufs && i <= n; ++i) {
+    volatile int dummy = 0;
+    mbar_wait(&bar_sfull[(int)((n - i) % kI8ScaleBufs)], (uint32_t)(((n - i) / kI8ScaleBufs) & 1), limit_ns, &dummy,
+              site);
+  }
 }
 
 // First row and number of rows of group g, kept inside [0, R).
@@ -197,7 +221,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   __shared__ int s_grows[kMaxGroupsSmem];
   constexpr int PARTS = OUTN >= 64 ? 4 : OUTN / 16;   // epilogue warps per TMEM quarter that have columns
   constexpr int CW = OUTN / PARTS;                    // output columns of such a warp, in chunks of 16
-  __shared__ __align__(16) float s_scale[4 * PARTS][kGLU ? 2 * CW : CW];
+  // channel scales of the tiles in flight (gate, then up): copied in by the producer ahead of a tile's operands, so
+  // that the epilogue never waits for global memory
+  __shared__ __align__(16) float s_scale[kI8ScaleBufs][BN];
+  __shared__ __align__(8) uint64_t bar_sfull[kI8ScaleBufs], bar_sempty[kI8ScaleBufs];
 
   const int warp = warp_id(), lane = lane_id();
   const int crank = kPair ? (int)cluster_ctarank() : 0;   // 0 = leader of the pair
@@ -211,6 +238,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(&bar_full[s], 1); mbar_init(&bar_empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&bar_tfull[a], 1); mbar_init(&bar_tempty[a], CG * 4 * PARTS); }
+    for (int b = 0; b < kI8ScaleBufs; ++b) { mbar_init(&bar_sfull[b], 1); mbar_init(&bar_sempty[b], 4 * PARTS); }
     mbar_init(&bar_final, 1);
     s_abort = 0;
     fence_mbar_init();
@@ -252,11 +280,22 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     // ------------------------------------------------ TMA producer
     int stage = 0;
     uint32_t phase = 0;
-    long long issued = 0;
+    long long issued = 0, scales = 0;
     if (lane == 0) {
       for (long long tile = unit; tile < total && !s_abort; tile += n_units) {
         int g, row0, rows_left, n0;
         locate(tile, g, row0, rows_left, n0);
+        {
+          const int b = (int)(scales % kI8ScaleBufs);
+          const uint32_t ph = (uint32_t)((scales / kI8ScaleBufs) & 1);
+          if (!mbar_wait(&bar_sempty[b], ph ^ 1u, p.wait_limit_ns, &s_abort, 0x0507)) break;
+          const uint32_t n = (uint32_t)min(OUTN, p.N - n0) * 4;   // a multiple of 64 bytes
+          const float* src = p.b_scale + (size_t)g * p.b_rows + n0;
+          mbar_arrive_expect_tx(&bar_sfull[b], kGLU ? 2 * n : n);
+          bulk_load(&s_scale[b][0], src, n, &bar_sfull[b]);
+          if (kGLU) bulk_load(&s_scale[b][OUTN], src + p.up_row0, n, &bar_sfull[b]);
+          ++scales;
+        }
         const int na = loaded(rows_left - crank * kBM);
         const int na_all = kPair ? loaded(rows_left) + loaded(rows_left - kBM) : na;
         const uint32_t bytes = (uint32_t)(na_all * kI8BK + CG * Cfg::kBBytes);
@@ -300,6 +339,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           mbar_wait(&bar_full[(int)(n % S)], (uint32_t)((n / S) & 1), p.wait_limit_ns, &dummy, 0x0502);
         }
       }
+      i8_drain_scales(bar_sfull, scales, p.wait_limit_ns, 0x0508);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -344,39 +384,43 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     const int ew = warp - 4;
     const int q = warp & 3;                 // TMEM lane quarter: this warp's 32 accumulator rows
     const int c_base = (ew >> 2) * CW;      // this warp's first output column in the tile
-    float* scl = s_scale[ew];
+    const int row = q * 32 + lane;
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (long long tile = unit; tile < total && !s_abort; tile += n_units) {
-      int g, row0, rows_left, n0;
+    long long n_tile = 0;
+    int g, row0 = 0, rows_left = 0, n0 = 0;
+    float sx = 0.f;                         // this lane's token scale, loaded a tile ahead
+    auto fetch = [&](long long tile) {
+      if (tile >= total) return;
       locate(tile, g, row0, rows_left, n0);
-      const int row = q * 32 + lane;
+      sx = row < rows_left - crank * kBM ? p.a_scale[(long long)row0 + row] : 0.f;
+    };
+    fetch(unit);
+    for (long long tile = unit; tile < total && !s_abort; tile += n_units, ++n_tile) {
       const bool live = row < rows_left - crank * kBM;
-      // this warp's channel scales (gate, then up) and this lane's token scale, while the MMAs run
-      {
-        const float* bs = p.b_scale + (size_t)g * p.b_rows;
-        for (int c = lane; c < CW; c += 32) {
-          const int col = n0 + c_base + c;
-          scl[c] = col < p.N ? bs[col] : 0.f;
-          if (kGLU) scl[CW + c] = col < p.N ? bs[p.up_row0 + col] : 0.f;
-        }
-      }
-      const float sx = live ? p.a_scale[(long long)row0 + row] : 0.f;
+      const float sxc = sx;
       __nv_bfloat16* out = p.out + ((long long)row0 + row) * p.N + n0 + c_base;
       const int cols = p.N - n0 - c_base;   // N is a multiple of 16: whole chunks
-      __syncwarp();
+      fetch(tile + n_units);
+      const int sb = (int)(n_tile % kI8ScaleBufs);
+      if (!mbar_wait(&bar_sfull[sb], (uint32_t)((n_tile / kI8ScaleBufs) & 1), p.wait_limit_ns, &s_abort, 0x0509)) break;
+      const float* scl = &s_scale[sb][c_base];
       if (!mbar_wait(&bar_tfull[acc], acc_phase, p.wait_limit_ns, &s_abort, 0x0506)) break;
       tc_fence_after();
       const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN + c_base);
+      // chunks of 16 columns; the next chunk's loads are in flight while one is worked on
+      uint32_t v[2][16], u[2][kGLU ? 16 : 1];
+      tmem_ld16(t_row, v[0]);
+      if constexpr (kGLU) tmem_ld16(t_row + OUTN, u[0]);
 #pragma unroll
       for (int c0 = 0; c0 < CW; c0 += 16) {
-        uint32_t v[16];
-        uint32_t u[kGLU ? 16 : 1];
-        tmem_ld16(t_row + c0, v);
-        if constexpr (kGLU) tmem_ld16(t_row + OUTN + c0, u);
+        const int b = (c0 / 16) & 1;
         tmem_ld_wait();
-        if (c0 + 16 == CW) {   // the accumulator is drained: one arrival per epilogue warp (on the leader)
+        if (c0 + 16 < CW) {
+          tmem_ld16(t_row + c0 + 16, v[b ^ 1]);
+          if constexpr (kGLU) tmem_ld16(t_row + OUTN + c0 + 16, u[b ^ 1]);
+        } else {   // the accumulator is drained: one arrival per epilogue warp (on the leader)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -388,21 +432,20 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 sg = *reinterpret_cast<const float4*>(scl + c0 + i);
-          const float gs[4] = {sg.x, sg.y, sg.z, sg.w};
-          float f[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = (float)(int)v[i + j] * sx * gs[j];
+          float2 f0 = i8_scaled(v[b][i], v[b][i + 1], sxc, sg.x, sg.y);
+          float2 f1 = i8_scaled(v[b][i + 2], v[b][i + 3], sxc, sg.z, sg.w);
           if constexpr (kGLU) {
-            const float4 su = *reinterpret_cast<const float4*>(scl + CW + c0 + i);
-            const float us[4] = {su.x, su.y, su.z, su.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = i8_act<MODE>(f[j]) * ((float)(int)u[i + j] * sx * us[j]);
+            const float4 su = *reinterpret_cast<const float4*>(scl + OUTN + c0 + i);
+            f0 = i8_glu2<MODE>(f0, i8_scaled(u[b][i], u[b][i + 1], sxc, su.x, su.y));
+            f1 = i8_glu2<MODE>(f1, i8_scaled(u[b][i + 2], u[b][i + 3], sxc, su.z, su.w));
           }
-          o[i / 2] = pack_bf16x2(f[0], f[1]);
-          o[i / 2 + 1] = pack_bf16x2(f[2], f[3]);
+          o[i / 2] = pack_bf16x2(f0.x, f0.y);
+          o[i / 2 + 1] = pack_bf16x2(f1.x, f1.y);
         }
         if (live && c0 < cols) st_row16(out + c0, o, wide);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_sempty[sb]);
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
   }

@@ -828,11 +828,15 @@ static int launch_i8_fused_t(const I8Params& p, const void* xq, const void* w13,
   if (rc) return rc;
   rc = make_map_i8(&t2, w2, 3, d2, CG == 2 ? 128 : 256);
   if (rc) return rc;
+  CUtensorMap ty;
+  const cuuint64_t dy[2] = {(cuuint64_t)p.N, (cuuint64_t)p.R};
+  rc = make_map(&ty, p.out, 2, dy, 32);
+  if (rc) return rc;
   const long long TM = (long long)kBM * CG;
   const long long tiles = p.group_rows ? (p.R / TM + p.n_groups) : cdiv(p.R, TM);
   const int units = (int)std::max<long long>(1, std::min<long long>(num_sms() / CG, tiles));
   MOE_CUDA_TRY(launch_pdl(k_int8_fused<MODE, H, CG>, dim3((unsigned)(CG * units)), dim3(kI8Threads), Cfg::kSmemBytes,
-                          st, (unsigned)CG, tx, txf, t13, t2, p, s2));
+                          st, (unsigned)CG, tx, txf, t13, t2, ty, p, s2));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
