@@ -18,7 +18,8 @@
 // MMA that reads them.  The epilogue is what the kernel waits for, so it is kept lean: channel scales come by bulk
 // copies of the producer, y leaves through shared memory by TMA (a warp's 32 rows x 64 columns at a time; stores from
 // registers touch 32 lines each and held up the fence before the codes are published), and warps without rows skip
-// the arithmetic.  Roles as k_int8_gemm: warp 0 TMA, warp 1 MMA, warps 4-19 epilogue.
+// the arithmetic.  Roles as k_int8_gemm: warps 0, 2, 3 copies, warp 1 MMA,
+// warps 4-19 epilogue.
 #pragma once
 
 #include "int8_gemm.cuh"
@@ -60,7 +61,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   // h codes [128 columns][128 rows][128 B], y staging [16 warps][32 rows][128 B] (both swizzled), ring
   uint8_t* stage_y = smem + Cfg::kHBytes;
   uint8_t* ring = stage_y + Cfg::kOutBytes;
-  __shared__ __align__(8) uint64_t bar_full[S], bar_empty[S], bar_tfull[2], bar_tempty[2], bar_hready, bar_final;
+  __shared__ __align__(8) uint64_t bar_full[S], bar_empty[S], bar_tfull[2], bar_tempty[2], bar_final;
+  // h codes written: by this CTA's epilogue warps, and (on the leader) by the pair's other CTA
+  __shared__ __align__(8) uint64_t bar_hlocal, bar_hpeer;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_prefix[kMaxGroupsSmem + 1];
@@ -79,14 +82,15 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int nd = (p.N + 255) / 256;                 // down jobs per tile
   const int G = p.group_rows == nullptr ? 1 : p.n_groups;
 
-  if (warp == 2) i8_group_table(p, TM, s_prefix, s_gstart, s_grows);
+  if (warp == 3) i8_group_table(p, TM, s_prefix, s_gstart, s_grows);
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(&bar_full[s], 1); mbar_init(&bar_empty[s], 1); }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&bar_tfull[a], 1);
       mbar_init(&bar_tempty[a], CG * kI8EpiWarps);
     }
-    mbar_init(&bar_hready, CG * kI8EpiWarps);
+    mbar_init(&bar_hlocal, kI8EpiWarps);
+    mbar_init(&bar_hpeer, 1);
     for (int b = 0; b < kI8ScaleBufs; ++b) { mbar_init(&bar_sfull[b], 1); mbar_init(&bar_sempty[b], kI8EpiWarps); }
     mbar_init(&bar_final, 1);
     s_abort = 0;
@@ -122,45 +126,26 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     rows_left = s_grows[g] - m_tile;
   };
 
+  // As in k_int8_gemm the copies are dealt to three warps.  Each walks the jobs in the same order.
   if (warp == 0) {
-    // ------------------------------------------------ TMA producer
+    // ------------------------------------------------ x tiles, and the byte counts of every slot
     if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      long long issued = 0, scales = 0;
+      RingPos<S> r;
+      long long issued = 0;
+      bool ok = true;
+      const uint32_t fb0 = kPair ? mapa_shared(smem_u32(&bar_full[0]), 0) : 0;
       auto loaded = [](int rows) {
         return rows <= 0 ? 0 : rows > kI8Few ? kBM : (rows + kI8ABox - 1) / kI8ABox * kI8ABox;
       };
       // waits for the slot and arms it; false when a wait gave up
       auto arm = [&](uint32_t bytes) {
-        if (!mbar_wait(&bar_empty[stage], phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0601)) return false;
-        if (crank == 0) mbar_arrive_expect_tx(&bar_full[stage], bytes);
+        if (!mbar_wait(&bar_empty[r.stage], r.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0601)) return false;
+        if (crank == 0) mbar_arrive_expect_tx(&bar_full[r.stage], bytes);
         return true;
       };
-      auto next = [&]() {
-        ++issued;
-        if (++stage == S) { stage = 0; phase ^= 1u; }
-      };
-      auto load_b = [&](uint8_t* dst, const CUtensorMap* map, int k0, int row, int g) {
-        if (kPair) tma_load_3d_pair(dst, map, mapa_shared(smem_u32(&bar_full[stage]), 0), k0, row, g);
-        else tma_load_3d(dst, map, &bar_full[stage], k0, row, g);
-      };
-      // a job's channel scales: n floats of a (and of b, behind 128 floats)
-      auto load_scales = [&](const float* a, const float* b, int n) {
-        const int k = (int)(scales % kI8ScaleBufs);
-        if (!mbar_wait(&bar_sempty[k], (uint32_t)((scales / kI8ScaleBufs) & 1) ^ 1u, p.wait_limit_ns, &s_abort, 0x0609))
-          return false;
-        mbar_arrive_expect_tx(&bar_sfull[k], (uint32_t)n * (b != nullptr ? 8u : 4u));
-        bulk_load(&s_scale[k][0], a, (uint32_t)n * 4, &bar_sfull[k]);
-        if (b != nullptr) bulk_load(&s_scale[k][128], b, (uint32_t)n * 4, &bar_sfull[k]);
-        ++scales;
-        return true;
-      };
-      bool ok = true;
       for (int i = 0; i <= mine && ok && !s_abort; ++i) {
-        int g = 0, row0 = 0, rows_left = 0, gd = 0, rd, ld;
+        int g, row0 = 0, rows_left = 0;
         if (i < mine) locate(i, g, row0, rows_left);
-        if (i > 0) locate(i - 1, gd, rd, ld);
         const int na = loaded(rows_left - crank * kBM);
         const int na_all = kPair ? loaded(rows_left) + loaded(rows_left - kBM) : na;
         const uint32_t bytes = (uint32_t)(na_all * kI8BK + CG * Cfg::kBBytes);
@@ -169,35 +154,21 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         for (int jd = 0; jd < nd && ok; ++jd) {
           for (int job = 0; job < NGU && ok; ++job) {
             if (i == mine || job * nd / NGU != jd) continue;
-            const float* s13 = p.b_scale + (size_t)g * (2 * H) + 128 * job;
-            ok = load_scales(s13, s13 + H, 128);
-            for (int kb = 0; ok && kb < nk; ++kb) {
+            for (int k0 = 0; k0 < p.K; k0 += kI8BK) {
               if (!(ok = arm(bytes))) break;
-              uint8_t* a_s = ring + (size_t)stage * Cfg::kSlotBytes;
-              uint8_t* b_s = a_s + Cfg::kABytes;
-              for (int r = 0; r < na; r += step) {
-                if (kPair)
-                  tma_load_2d_pair(a_s + r * kI8BK, mx, mapa_shared(smem_u32(&bar_full[stage]), 0), kb * kI8BK,
-                                   row0 + r);
-                else
-                  tma_load_2d(a_s + r * kI8BK, mx, &bar_full[stage], kb * kI8BK, row0 + r);
+              uint8_t* a_s = ring + (size_t)r.stage * Cfg::kSlotBytes;
+              for (int n = 0; n < na; n += step) {
+                if (kPair) tma_load_2d_pair(a_s + n * kI8BK, mx, fb0 + 8 * r.stage, k0, row0 + n);
+                else tma_load_2d(a_s + n * kI8BK, mx, &bar_full[r.stage], k0, row0 + n);
               }
-              if (kPair) {
-                load_b(b_s, &tmW13, kb * kI8BK, (crank == 0 ? 0 : H) + 128 * job, g);
-              } else {
-                load_b(b_s, &tmW13, kb * kI8BK, 128 * job, g);
-                load_b(b_s + 128 * kI8BK, &tmW13, kb * kI8BK, H + 128 * job, g);
-              }
-              next();
+              ++issued;
+              r.next();
             }
           }
-          if (i > 0 && ok) ok = load_scales(s2 + (size_t)gd * p.N + 256 * jd, nullptr, min(256, p.N - 256 * jd));
           for (int kb = 0; i > 0 && ok && kb < NKD; kb += Cfg::kDownSteps) {
             if (!(ok = arm((uint32_t)(CG * Cfg::kDownSteps * Cfg::kBBytes)))) break;
-            uint8_t* b_s = ring + (size_t)stage * Cfg::kSlotBytes;
-            for (int j = 0; j < Cfg::kDownSteps; ++j)
-              load_b(b_s + j * Cfg::kBBytes, &tmW2, (kb + j) * kI8BK, 256 * jd + 128 * crank, gd);
-            next();
+            ++issued;
+            r.next();
           }
         }
       }
@@ -210,40 +181,108 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           mbar_wait(&bar_full[(int)(n % S)], (uint32_t)((n / S) & 1), p.wait_limit_ns, &dummy, 0x0602);
         }
       }
-      i8_drain_scales(bar_sfull, scales, p.wait_limit_ns, 0x060A);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------ weight tiles
+    if (lane == 0) {
+      RingPos<S> r;
+      bool ok = true;
+      const uint32_t fb0 = kPair ? mapa_shared(smem_u32(&bar_full[0]), 0) : 0;
+      auto empty = [&]() { return mbar_wait(&bar_empty[r.stage], r.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x060E); };
+      auto load_b = [&](uint8_t* dst, const CUtensorMap* map, int k0, int row, int g) {
+        if (kPair) tma_load_3d_pair(dst, map, fb0 + 8 * r.stage, k0, row, g);
+        else tma_load_3d(dst, map, &bar_full[r.stage], k0, row, g);
+      };
+      int g = 0, gd = 0;
+      for (int i = 0; i <= mine && ok && !s_abort; ++i) {
+        int row0, rows_left;
+        gd = g;
+        if (i < mine) locate(i, g, row0, rows_left);
+        for (int jd = 0; jd < nd && ok; ++jd) {
+          for (int job = 0; job < NGU && ok; ++job) {
+            if (i == mine || job * nd / NGU != jd) continue;
+            for (int k0 = 0; k0 < p.K; k0 += kI8BK) {
+              if (!(ok = empty())) break;
+              uint8_t* b_s = ring + (size_t)r.stage * Cfg::kSlotBytes + Cfg::kABytes;
+              if (kPair) {
+                load_b(b_s, &tmW13, k0, (crank == 0 ? 0 : H) + 128 * job, g);
+              } else {
+                load_b(b_s, &tmW13, k0, 128 * job, g);
+                load_b(b_s + 128 * kI8BK, &tmW13, k0, H + 128 * job, g);
+              }
+              r.next();
+            }
+          }
+          for (int kb = 0; i > 0 && ok && kb < NKD; kb += Cfg::kDownSteps) {
+            if (!(ok = empty())) break;
+            uint8_t* b_s = ring + (size_t)r.stage * Cfg::kSlotBytes;
+            for (int j = 0; j < Cfg::kDownSteps; ++j)
+              load_b(b_s + j * Cfg::kBBytes, &tmW2, (kb + j) * kI8BK, 256 * jd + 128 * crank, gd);
+            r.next();
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------ channel scales
+    if (lane == 0) {
+      RingPos<kI8ScaleBufs> r;
+      long long issued = 0;
+      bool ok = true;
+      // a job's channel scales: n floats of a (and of b, behind 128 floats)
+      auto load_scales = [&](const float* a, const float* b, int n) {
+        if (!mbar_wait(&bar_sempty[r.stage], r.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0609)) return false;
+        mbar_arrive_expect_tx(&bar_sfull[r.stage], (uint32_t)n * (b != nullptr ? 8u : 4u));
+        bulk_load(&s_scale[r.stage][0], a, (uint32_t)n * 4, &bar_sfull[r.stage]);
+        if (b != nullptr) bulk_load(&s_scale[r.stage][128], b, (uint32_t)n * 4, &bar_sfull[r.stage]);
+        ++issued;
+        r.next();
+        return true;
+      };
+      int g = 0, gd = 0;
+      for (int i = 0; i <= mine && ok && !s_abort; ++i) {
+        int row0, rows_left;
+        gd = g;
+        if (i < mine) locate(i, g, row0, rows_left);
+        for (int jd = 0; jd < nd && ok; ++jd) {
+          for (int job = 0; job < NGU && ok; ++job) {
+            if (i == mine || job * nd / NGU != jd) continue;
+            const float* s13 = p.b_scale + (size_t)g * (2 * H) + 128 * job;
+            ok = load_scales(s13, s13 + H, 128);
+          }
+          if (i > 0 && ok) ok = load_scales(s2 + (size_t)gd * p.N + 256 * jd, nullptr, min(256, p.N - 256 * jd));
+        }
+      }
+      i8_drain_scales(bar_sfull, issued, p.wait_limit_ns, 0x060A);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (leader CTA)
     if (lane == 0 && crank == 0) {
-      int stage = 0, slot = 0;
-      uint32_t phase = 0, slot_phase = 0;
-      const uint32_t h_addr = smem_u32(smem);
-      auto mma128 = [&](uint32_t d_tmem, uint32_t a_addr, uint32_t b_addr, bool first) {
-#pragma unroll
-        for (int kk = 0; kk < kI8BK / 32; ++kk)
-          tc_mma_i8<CG>(d_tmem, smem_desc_k128(a_addr + kk * 32), smem_desc_k128(b_addr + kk * 32), IDESC,
-                        (!first || kk > 0) ? 1u : 0u);
-      };
+      RingPos<S> r;
+      RingPos<2> acc;
+      const uint32_t h_addr = smem_u32(smem), ring_addr = smem_u32(ring);
       auto acquire = [&]() {
-        if (!mbar_wait(&bar_tempty[slot], slot_phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0603)) return false;
+        if (!mbar_wait(&bar_tempty[acc.stage], acc.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0603)) return false;
         tc_fence_after();
         return true;
       };
       auto full = [&]() {
-        if (!mbar_wait(&bar_full[stage], phase, p.wait_limit_ns, &s_abort, 0x0605)) return false;
+        if (!mbar_wait(&bar_full[r.stage], r.phase, p.wait_limit_ns, &s_abort, 0x0605)) return false;
         tc_fence_after();
         return true;
       };
       auto release_stage = [&]() {
-        if (kPair) tc_commit_pair_mc(&bar_empty[stage], 0x3);
-        else tc_commit(&bar_empty[stage]);
-        if (++stage == S) { stage = 0; phase ^= 1u; }
+        if (kPair) tc_commit_pair_mc(&bar_empty[r.stage], 0x3);
+        else tc_commit(&bar_empty[r.stage]);
+        r.next();
       };
       auto publish = [&]() {
-        if (kPair) tc_commit_pair_mc(&bar_tfull[slot], 0x3);
-        else tc_commit(&bar_tfull[slot]);
-        if (++slot == 2) { slot = 0; slot_phase ^= 1u; }
+        if (kPair) tc_commit_pair_mc(&bar_tfull[acc.stage], 0x3);
+        else tc_commit(&bar_tfull[acc.stage]);
+        acc.next();
       };
       bool ok = true;
       for (int i = 0; i <= mine && ok && !s_abort; ++i) {
@@ -252,30 +291,31 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           for (int job = 0; job < NGU && ok; ++job) {
             if (i == mine || job * nd / NGU != jd) continue;
             if (!(ok = acquire())) break;
-            const uint32_t d_tmem = tmem_base + (uint32_t)(slot * 256);
+            const uint32_t d_tmem = tmem_base + (uint32_t)(acc.stage * 256);
             for (int kb = 0; kb < nk; ++kb) {
               if (!(ok = full())) break;
-              const uint32_t a_addr = smem_u32(ring + (size_t)stage * Cfg::kSlotBytes);
-              mma128(d_tmem, a_addr, a_addr + Cfg::kABytes, kb == 0);
+              const uint32_t a_addr = ring_addr + (uint32_t)(r.stage * Cfg::kSlotBytes);
+              i8_mma_step<CG>(d_tmem, a_addr, a_addr + Cfg::kABytes, IDESC, kb == 0);
               release_stage();
             }
             if (ok) publish();
           }
           if (i == 0 || !ok) continue;
           if (jd == 0) {   // h codes of tile t, written by both CTAs' epilogues
-            ok = mbar_wait_cluster(&bar_hready, (uint32_t)(t & 1), p.wait_limit_ns, &s_abort, 0x0604);
+            ok = mbar_wait(&bar_hlocal, (uint32_t)(t & 1), p.wait_limit_ns, &s_abort, 0x0604);
+            if (kPair) ok = ok && mbar_wait_cluster(&bar_hpeer, (uint32_t)(t & 1), p.wait_limit_ns, &s_abort, 0x060C);
             if (!ok) break;
             tc_fence_after();
           }
           if (!(ok = acquire())) break;
-          const uint32_t d_tmem = tmem_base + (uint32_t)(slot * 256);
+          const uint32_t d_tmem = tmem_base + (uint32_t)(acc.stage * 256);
           for (int kb = 0; kb < NKD; kb += Cfg::kDownSteps) {
             if (!(ok = full())) break;
-            const uint32_t b_addr = smem_u32(ring + (size_t)stage * Cfg::kSlotBytes);
+            const uint32_t b_addr = ring_addr + (uint32_t)(r.stage * Cfg::kSlotBytes);
 #pragma unroll
             for (int j = 0; j < Cfg::kDownSteps; ++j)
-              mma128(d_tmem, h_addr + (uint32_t)((kb + j) * (kBM * 128)),
-                     b_addr + (uint32_t)(j * Cfg::kBBytes), kb + j == 0);
+              i8_mma_step<CG>(d_tmem, h_addr + (uint32_t)((kb + j) * (kBM * 128)), b_addr + (uint32_t)(j * Cfg::kBBytes),
+                              IDESC, kb + j == 0);
             release_stage();
           }
           if (ok) publish();
@@ -285,6 +325,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       else tc_commit(&bar_final);
       volatile int dummy = 0;
       mbar_wait(&bar_final, 0, p.wait_limit_ns, &dummy, 0x0606);
+    }
+    // The other CTA of a pair passes its epilogue's "h ready" on to the leader.  A release at cluster scope took each
+    // epilogue warp about 3500 cycles a tile while stores were under way; here nothing waits for it but the MMAs.
+    if (kPair && lane == 0 && crank == 1) {
+      for (int t = 0; t < mine; ++t) {
+        if (!mbar_wait_cluster(&bar_hlocal, (uint32_t)(t & 1), p.wait_limit_ns, &s_abort, 0x060D)) break;
+        mbar_arrive_cluster_release(mapa_shared(smem_u32(&bar_hpeer), 0));
+      }
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -471,10 +519,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         fence_proxy_async_smem();   // the tensor core reads them through the async proxy
       }
       __syncwarp();
-      if (lane == 0) {
-        if (kPair) mbar_arrive_cluster_release(mapa_shared(smem_u32(&bar_hready), 0));
-        else mbar_arrive(&bar_hready);
-      }
+      if (lane == 0) mbar_arrive(&bar_hlocal);
     }
     if (kPair && lane == 0) bulk_wait_all();
   }

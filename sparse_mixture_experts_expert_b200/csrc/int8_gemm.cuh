@@ -8,8 +8,8 @@
 //   down (plain): writes y in bf16.
 // ExpertMesh README (grouped routed-expert products of quantised weights in [expert, output, input] order).
 //
-// Structure as k_grouped_gemm: persistent CTAs, warp 0 feeds A and B tiles of 128 bytes of K by TMA into a ring,
-// warp 1 issues tcgen05.mma (M = 128, or 256 over a CTA pair; four MMAs of K = 32 per stage), and the epilogue drains
+// Structure as k_grouped_gemm: persistent CTAs, warps 0 and 2 feed A and B tiles of 128 bytes of K by TMA into a ring,
+// warp 3 the channel scales, warp 1 issues tcgen05.mma (M = 128, or 256 over a CTA pair; four MMAs of K = 32 per stage), and the epilogue drains
 // one accumulator while the next one fills.  A k-step holds twice the inputs of a bf16 one for the same bytes and the
 // same MMA time, so a tile's main loop takes half as long and the epilogue weighs twice as much: sixteen epilogue warps
 // (four per TMEM quarter, each on a quarter of the columns) instead of four, and rows stored straight from the
@@ -86,6 +86,26 @@ __device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+
+// One k-step: four MMAs of K = 32 over the 128-byte rows at the two shared addresses (1024-byte aligned).
+template <int CG>
+__device__ __forceinline__ void i8_mma_step(uint32_t d_tmem, uint32_t a_addr, uint32_t b_addr, uint32_t idesc,
+                                            bool first) {
+  const uint64_t a = smem_desc_k128(a_addr), b = smem_desc_k128(b_addr);   // + 2: 32 bytes on
+  tc_mma_i8<CG>(d_tmem, a, b, idesc, first ? 0u : 1u);
+#pragma unroll
+  for (int kk = 1; kk < kI8BK / 32; ++kk) tc_mma_i8<CG>(d_tmem, a + 2 * kk, b + 2 * kk, idesc, 1u);
+}
+
+// Position in a ring of S stages: index, phase parity.
+template <int S>
+struct RingPos {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == S) { stage = 0; phase ^= 1u; }
+  }
+};
 
 // 16 bf16 values of a row: one 32-byte sector per lane in one store where the output lies on 32-byte boundaries
 // (`wide`, the same for the whole output: its rows are multiples of 32 bytes), else two of 16 bytes.
@@ -234,7 +254,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int nk = (p.K + kI8BK - 1) / kI8BK;
   const int G = p.group_rows == nullptr ? 1 : p.n_groups;
 
-  if (warp == 2) i8_group_table(p, TM, s_prefix, s_gstart, s_grows);
+  if (warp == 3) i8_group_table(p, TM, s_prefix, s_gstart, s_grows);
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(&bar_full[s], 1); mbar_init(&bar_empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&bar_tfull[a], 1); mbar_init(&bar_tempty[a], CG * 4 * PARTS); }
@@ -276,58 +296,38 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     return rows <= 0 ? 0 : rows > kI8Few ? kBM : (rows + kI8ABox - 1) / kI8ABox * kI8ABox;
   };
 
+  // The copies are dealt to three warps (A and the byte counts, B, channel scales): one thread's chain of waits and
+  // copies, in an SM whose issue slots the epilogue fills, took longer per k-step than the MMAs.
   if (warp == 0) {
-    // ------------------------------------------------ TMA producer
-    int stage = 0;
-    uint32_t phase = 0;
-    long long issued = 0, scales = 0;
+    // ------------------------------------------------ A tiles
     if (lane == 0) {
-      for (long long tile = unit; tile < total && !s_abort; tile += n_units) {
+      RingPos<S> r;
+      long long issued = 0;
+      bool ok = true;
+      const uint32_t fb0 = kPair ? mapa_shared(smem_u32(&bar_full[0]), 0) : 0;
+      for (long long tile = unit; tile < total && ok && !s_abort; tile += n_units) {
         int g, row0, rows_left, n0;
         locate(tile, g, row0, rows_left, n0);
-        {
-          const int b = (int)(scales % kI8ScaleBufs);
-          const uint32_t ph = (uint32_t)((scales / kI8ScaleBufs) & 1);
-          if (!mbar_wait(&bar_sempty[b], ph ^ 1u, p.wait_limit_ns, &s_abort, 0x0507)) break;
-          const uint32_t n = (uint32_t)min(OUTN, p.N - n0) * 4;   // a multiple of 64 bytes
-          const float* src = p.b_scale + (size_t)g * p.b_rows + n0;
-          mbar_arrive_expect_tx(&bar_sfull[b], kGLU ? 2 * n : n);
-          bulk_load(&s_scale[b][0], src, n, &bar_sfull[b]);
-          if (kGLU) bulk_load(&s_scale[b][OUTN], src + p.up_row0, n, &bar_sfull[b]);
-          ++scales;
-        }
         const int na = loaded(rows_left - crank * kBM);
         const int na_all = kPair ? loaded(rows_left) + loaded(rows_left - kBM) : na;
         const uint32_t bytes = (uint32_t)(na_all * kI8BK + CG * Cfg::kBBytes);
-        bool ok = true;
-        for (int kb = 0; kb < nk; ++kb) {
-          uint8_t* a_s = smem + (size_t)stage * Cfg::kStageBytes;
-          uint8_t* b_s = a_s + Cfg::kABytes;
-          ok = mbar_wait(&bar_empty[stage], phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0501);
-          if (!ok) break;
+        for (int k0 = 0; k0 < p.K; k0 += kI8BK) {
+          uint8_t* a_s = smem + (size_t)r.stage * Cfg::kStageBytes;
+          if (!(ok = mbar_wait(&bar_empty[r.stage], r.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0501))) break;
           // the leader's barrier counts the bytes of both CTAs of a pair
-          if (crank == 0) mbar_arrive_expect_tx(&bar_full[stage], bytes);
-          if (kPair) {
-            const uint32_t fb = mapa_shared(smem_u32(&bar_full[stage]), 0);
-            if (na == kBM) tma_load_2d_pair(a_s, &tmA, fb, kb * kI8BK, row0);
-            else
-              for (int i = 0; i < na; i += kI8ABox)
-                tma_load_2d_pair(a_s + i * kI8BK, &tmAFew, fb, kb * kI8BK, row0 + i);
-            const int brow = kGLU ? (crank == 0 ? n0 : p.up_row0 + n0) : n0 + crank * (BN / 2);
-            tma_load_3d_pair(b_s, &tmB, fb, kb * kI8BK, brow, g);
+          if (crank == 0) mbar_arrive_expect_tx(&bar_full[r.stage], bytes);
+          if (na == kBM) {
+            if (kPair) tma_load_2d_pair(a_s, &tmA, fb0 + 8 * r.stage, k0, row0);
+            else tma_load_2d(a_s, &tmA, &bar_full[r.stage], k0, row0);
           } else {
-            if (na == kBM) tma_load_2d(a_s, &tmA, &bar_full[stage], kb * kI8BK, row0);
-            else
-              for (int i = 0; i < na; i += kI8ABox)
-                tma_load_2d(a_s + i * kI8BK, &tmAFew, &bar_full[stage], kb * kI8BK, row0 + i);
-            tma_load_3d(b_s, &tmB, &bar_full[stage], kb * kI8BK, n0, g);
-            if (kGLU)
-              tma_load_3d(b_s + (BN / 2) * kI8BK, &tmB, &bar_full[stage], kb * kI8BK, p.up_row0 + n0, g);
+            for (int i = 0; i < na; i += kI8ABox) {
+              if (kPair) tma_load_2d_pair(a_s + i * kI8BK, &tmAFew, fb0 + 8 * r.stage, k0, row0 + i);
+              else tma_load_2d(a_s + i * kI8BK, &tmAFew, &bar_full[r.stage], k0, row0 + i);
+            }
           }
           ++issued;
-          if (++stage == S) { stage = 0; phase ^= 1u; }
+          r.next();
         }
-        if (!ok) break;
       }
       // No copy may still be landing in shared memory when the CTA ends (in a pair the leader's barriers count
       // both CTAs' copies; the pair leaves together).
@@ -339,38 +339,77 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           mbar_wait(&bar_full[(int)(n % S)], (uint32_t)((n / S) & 1), p.wait_limit_ns, &dummy, 0x0502);
         }
       }
-      i8_drain_scales(bar_sfull, scales, p.wait_limit_ns, 0x0508);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------ B tiles
+    if (lane == 0) {
+      RingPos<S> r;
+      bool ok = true;
+      const uint32_t fb0 = kPair ? mapa_shared(smem_u32(&bar_full[0]), 0) : 0;
+      for (long long tile = unit; tile < total && ok && !s_abort; tile += n_units) {
+        int g, row0, rows_left, n0;
+        locate(tile, g, row0, rows_left, n0);
+        const int brow = !kPair ? n0 : kGLU ? (crank == 0 ? n0 : p.up_row0 + n0) : n0 + crank * (BN / 2);
+        for (int k0 = 0; k0 < p.K; k0 += kI8BK) {
+          uint8_t* b_s = smem + (size_t)r.stage * Cfg::kStageBytes + Cfg::kABytes;
+          if (!(ok = mbar_wait(&bar_empty[r.stage], r.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x050A))) break;
+          if (kPair) {
+            tma_load_3d_pair(b_s, &tmB, fb0 + 8 * r.stage, k0, brow, g);
+          } else {
+            tma_load_3d(b_s, &tmB, &bar_full[r.stage], k0, brow, g);
+            if (kGLU)
+              tma_load_3d(b_s + (BN / 2) * kI8BK, &tmB, &bar_full[r.stage], k0, p.up_row0 + n0, g);
+          }
+          r.next();
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------ channel scales
+    if (lane == 0) {
+      RingPos<kI8ScaleBufs> r;
+      long long issued = 0;
+      for (long long tile = unit; tile < total && !s_abort; tile += n_units) {
+        int g, row0, rows_left, n0;
+        locate(tile, g, row0, rows_left, n0);
+        if (!mbar_wait(&bar_sempty[r.stage], r.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0507)) break;
+        const uint32_t n = (uint32_t)min(OUTN, p.N - n0) * 4;   // a multiple of 64 bytes
+        const float* src = p.b_scale + (size_t)g * p.b_rows + n0;
+        mbar_arrive_expect_tx(&bar_sfull[r.stage], kGLU ? 2 * n : n);
+        bulk_load(&s_scale[r.stage][0], src, n, &bar_sfull[r.stage]);
+        if (kGLU) bulk_load(&s_scale[r.stage][OUTN], src + p.up_row0, n, &bar_sfull[r.stage]);
+        ++issued;
+        r.next();
+      }
+      i8_drain_scales(bar_sfull, issued, p.wait_limit_ns, 0x0508);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
     if (lane == 0 && crank == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      for (long long tile = unit; tile < total && !s_abort; tile += n_units) {
-        if (!mbar_wait(&bar_tempty[acc], acc_phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0503)) break;
+      RingPos<S> r;
+      RingPos<2> acc;
+      bool ok = true;
+      const uint32_t base = smem_u32(smem);
+      for (long long tile = unit; tile < total && ok && !s_abort; tile += n_units) {
+        if (!mbar_wait(&bar_tempty[acc.stage], acc.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0503)) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-        bool ok = true;
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc.stage * BN);
         for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(&bar_full[stage], phase, p.wait_limit_ns, &s_abort, 0x0504)) { ok = false; break; }
+          if (!(ok = mbar_wait(&bar_full[r.stage], r.phase, p.wait_limit_ns, &s_abort, 0x0504))) break;
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + (size_t)stage * Cfg::kStageBytes);
-          const uint32_t b_addr = a_addr + Cfg::kABytes;
-#pragma unroll
-          for (int kk = 0; kk < kI8BK / 32; ++kk)
-            tc_mma_i8<CG>(d_tmem, smem_desc_k128(a_addr + kk * 32), smem_desc_k128(b_addr + kk * 32), IDESC,
-                          (kb > 0 || kk > 0) ? 1u : 0u);
-          if (kPair) tc_commit_pair_mc(&bar_empty[stage], 0x3);
-          else tc_commit(&bar_empty[stage]);
-          if (++stage == S) { stage = 0; phase ^= 1u; }
+          const uint32_t a_addr = base + (uint32_t)(r.stage * Cfg::kStageBytes);
+          i8_mma_step<CG>(d_tmem, a_addr, a_addr + Cfg::kABytes, IDESC, kb == 0);
+          if (kPair) tc_commit_pair_mc(&bar_empty[r.stage], 0x3);
+          else tc_commit(&bar_empty[r.stage]);
+          r.next();
         }
         if (!ok) break;
-        if (kPair) tc_commit_pair_mc(&bar_tfull[acc], 0x3);
-        else tc_commit(&bar_tfull[acc]);
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        if (kPair) tc_commit_pair_mc(&bar_tfull[acc.stage], 0x3);
+        else tc_commit(&bar_tfull[acc.stage]);
+        acc.next();
       }
       // all issued MMAs complete before TMEM is released
       if (kPair) tc_commit_pair(&bar_final);
