@@ -10,9 +10,9 @@
 // threads that share a row through shared memory, and the codes (128 bytes a row per 128 columns) are the A operand
 // of the down product as they lie.
 //
-// Order of work of one CTA (pair): the gate/up jobs of tile i + 1 spread between the down jobs of tile i, then the
-// codes of tile i + 1 (for d = 768, H = 256: G0 D0 G1 D1 D2 C).  The tensor core has the next tile's first gate/up job
-// to do while the epilogue makes the codes, and a gate/up job's long MMA loop runs beside the stores of a down job.
+// Order of work of one CTA (pair): the gate/up jobs of tile i + 1, the down jobs of tile i, the codes of tile i + 1 (for
+// d = 768, H = 256: G0 G1 D0 D1 D2 C).  The tensor core has the next tile's gate/up to do while the epilogue makes the
+// codes, and the epilogue has two finished gate/up accumulators when it is through with them.
 // Jobs alternate between two TMEM accumulators of 256 columns, so an epilogue overlaps the next job's MMAs.  The codes
 // of tile i + 1 replace those of tile i after the epilogue has seen tile i's last down accumulator, that is after every
 // MMA that reads them.  The epilogue is what the kernel waits for, so it is kept lean: channel scales come by bulk
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   __shared__ __align__(8) uint64_t bar_sfull[kI8ScaleBufs], bar_sempty[kI8ScaleBufs];
   __shared__ uint32_t s_top[2][4][kBM];             // partial row maxima of h, by tile parity
 
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = warp_id_uniform(), lane = lane_id();
   const int crank = kPair ? (int)cluster_ctarank() : 0;   // 0 = leader of the pair
   const int unit = kPair ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
   const int n_units = kPair ? (int)(gridDim.x >> 1) : (int)gridDim.x;
@@ -151,25 +151,22 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const uint32_t bytes = (uint32_t)(na_all * kI8BK + CG * Cfg::kBBytes);
         const CUtensorMap* mx = na == kBM ? &tmX : &tmXFew;
         const int step = na == kBM ? kBM : kI8ABox;
-        for (int jd = 0; jd < nd && ok; ++jd) {
-          for (int job = 0; job < NGU && ok; ++job) {
-            if (i == mine || job * nd / NGU != jd) continue;
-            for (int k0 = 0; k0 < p.K; k0 += kI8BK) {
-              if (!(ok = arm(bytes))) break;
-              uint8_t* a_s = ring + (size_t)r.stage * Cfg::kSlotBytes;
-              for (int n = 0; n < na; n += step) {
-                if (kPair) tma_load_2d_pair(a_s + n * kI8BK, mx, fb0 + 8 * r.stage, k0, row0 + n);
-                else tma_load_2d(a_s + n * kI8BK, mx, &bar_full[r.stage], k0, row0 + n);
-              }
-              ++issued;
-              r.next();
+        for (int job = 0; i < mine && ok && job < NGU; ++job) {
+          for (int k0 = 0; k0 < p.K; k0 += kI8BK) {
+            if (!(ok = arm(bytes))) break;
+            uint8_t* a_s = ring + (size_t)r.stage * Cfg::kSlotBytes;
+            for (int n = 0; n < na; n += step) {
+              if (kPair) tma_load_2d_pair(a_s + n * kI8BK, mx, fb0 + 8 * r.stage, k0, row0 + n);
+              else tma_load_2d(a_s + n * kI8BK, mx, &bar_full[r.stage], k0, row0 + n);
             }
-          }
-          for (int kb = 0; i > 0 && ok && kb < NKD; kb += Cfg::kDownSteps) {
-            if (!(ok = arm((uint32_t)(CG * Cfg::kDownSteps * Cfg::kBBytes)))) break;
             ++issued;
             r.next();
           }
+        }
+        for (int n = 0; i > 0 && ok && n < nd * (NKD / Cfg::kDownSteps); ++n) {   // W2 alone
+          if (!(ok = arm((uint32_t)(CG * Cfg::kDownSteps * Cfg::kBBytes)))) break;
+          ++issued;
+          r.next();
         }
       }
       // no copy may still be landing in shared memory when the CTA ends
@@ -199,21 +196,20 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         int row0, rows_left;
         gd = g;
         if (i < mine) locate(i, g, row0, rows_left);
-        for (int jd = 0; jd < nd && ok; ++jd) {
-          for (int job = 0; job < NGU && ok; ++job) {
-            if (i == mine || job * nd / NGU != jd) continue;
-            for (int k0 = 0; k0 < p.K; k0 += kI8BK) {
-              if (!(ok = empty())) break;
-              uint8_t* b_s = ring + (size_t)r.stage * Cfg::kSlotBytes + Cfg::kABytes;
-              if (kPair) {
-                load_b(b_s, &tmW13, k0, (crank == 0 ? 0 : H) + 128 * job, g);
-              } else {
-                load_b(b_s, &tmW13, k0, 128 * job, g);
-                load_b(b_s + 128 * kI8BK, &tmW13, k0, H + 128 * job, g);
-              }
-              r.next();
+        for (int job = 0; i < mine && ok && job < NGU; ++job) {
+          for (int k0 = 0; k0 < p.K; k0 += kI8BK) {
+            if (!(ok = empty())) break;
+            uint8_t* b_s = ring + (size_t)r.stage * Cfg::kSlotBytes + Cfg::kABytes;
+            if (kPair) {
+              load_b(b_s, &tmW13, k0, (crank == 0 ? 0 : H) + 128 * job, g);
+            } else {
+              load_b(b_s, &tmW13, k0, 128 * job, g);
+              load_b(b_s + 128 * kI8BK, &tmW13, k0, H + 128 * job, g);
             }
+            r.next();
           }
+        }
+        for (int jd = 0; jd < nd && ok; ++jd) {
           for (int kb = 0; i > 0 && ok && kb < NKD; kb += Cfg::kDownSteps) {
             if (!(ok = empty())) break;
             uint8_t* b_s = ring + (size_t)r.stage * Cfg::kSlotBytes;
@@ -246,13 +242,12 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         int row0, rows_left;
         gd = g;
         if (i < mine) locate(i, g, row0, rows_left);
+        for (int job = 0; i < mine && ok && job < NGU; ++job) {
+          const float* s13 = p.b_scale + (size_t)g * (2 * H) + 128 * job;
+          ok = load_scales(s13, s13 + H, 128);
+        }
         for (int jd = 0; jd < nd && ok; ++jd) {
-          for (int job = 0; job < NGU && ok; ++job) {
-            if (i == mine || job * nd / NGU != jd) continue;
-            const float* s13 = p.b_scale + (size_t)g * (2 * H) + 128 * job;
-            ok = load_scales(s13, s13 + H, 128);
-          }
-          if (i > 0 && ok) ok = load_scales(s2 + (size_t)gd * p.N + 256 * jd, nullptr, min(256, p.N - 256 * jd));
+          if (i > 0) ok = load_scales(s2 + (size_t)gd * p.N + 256 * jd, nullptr, min(256, p.N - 256 * jd));
         }
       }
       i8_drain_scales(bar_sfull, issued, p.wait_limit_ns, 0x060A);
@@ -260,53 +255,48 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (leader CTA)
-    if (lane == 0 && crank == 0) {
+    if (crank == 0) {
       RingPos<S> r;
       RingPos<2> acc;
-      const uint32_t h_addr = smem_u32(smem), ring_addr = smem_u32(ring);
+      const uint32_t lead = lane == 0, h_addr = smem_u32(smem), ring_addr = smem_u32(ring);
       auto acquire = [&]() {
-        if (!mbar_wait(&bar_tempty[acc.stage], acc.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0603)) return false;
+        if (!mbar_wait_warp(&bar_tempty[acc.stage], acc.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0603)) return false;
         tc_fence_after();
         return true;
       };
       auto full = [&]() {
-        if (!mbar_wait(&bar_full[r.stage], r.phase, p.wait_limit_ns, &s_abort, 0x0605)) return false;
+        if (!mbar_wait_warp(&bar_full[r.stage], r.phase, p.wait_limit_ns, &s_abort, 0x0605)) return false;
         tc_fence_after();
         return true;
       };
       auto release_stage = [&]() {
-        if (kPair) tc_commit_pair_mc(&bar_empty[r.stage], 0x3);
-        else tc_commit(&bar_empty[r.stage]);
+        tc_commit_i8<CG>(lead, &bar_empty[r.stage]);
         r.next();
       };
       auto publish = [&]() {
-        if (kPair) tc_commit_pair_mc(&bar_tfull[acc.stage], 0x3);
-        else tc_commit(&bar_tfull[acc.stage]);
+        tc_commit_i8<CG>(lead, &bar_tfull[acc.stage]);
         acc.next();
       };
       bool ok = true;
-      for (int i = 0; i <= mine && ok && !s_abort; ++i) {
-        const int t = i - 1;
+      for (int i = 0; i <= mine && ok; ++i) {
+        for (int job = 0; i < mine && ok && job < NGU; ++job) {
+          if (!(ok = acquire())) break;
+          const uint32_t d_tmem = tmem_base + (uint32_t)(acc.stage * 256);
+          for (int kb = 0; kb < nk; ++kb) {
+            if (!(ok = full())) break;
+            const uint32_t a_addr = ring_addr + (uint32_t)(r.stage * Cfg::kSlotBytes);
+            i8_mma_step<CG>(lead, d_tmem, a_addr, a_addr + Cfg::kABytes, IDESC, kb == 0);
+            release_stage();
+          }
+          if (ok) publish();
+        }
+        if (i == 0 || !ok) continue;
+        const uint32_t ph = (uint32_t)((i - 1) & 1);   // h codes of tile i - 1, written by both CTAs' epilogues
+        ok = mbar_wait_warp(&bar_hlocal, ph, p.wait_limit_ns, &s_abort, 0x0604);
+        if (kPair && ok)
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&bar_hpeer, ph, p.wait_limit_ns, &s_abort, 0x060C)) != 0;
+        tc_fence_after();
         for (int jd = 0; jd < nd && ok; ++jd) {
-          for (int job = 0; job < NGU && ok; ++job) {
-            if (i == mine || job * nd / NGU != jd) continue;
-            if (!(ok = acquire())) break;
-            const uint32_t d_tmem = tmem_base + (uint32_t)(acc.stage * 256);
-            for (int kb = 0; kb < nk; ++kb) {
-              if (!(ok = full())) break;
-              const uint32_t a_addr = ring_addr + (uint32_t)(r.stage * Cfg::kSlotBytes);
-              i8_mma_step<CG>(d_tmem, a_addr, a_addr + Cfg::kABytes, IDESC, kb == 0);
-              release_stage();
-            }
-            if (ok) publish();
-          }
-          if (i == 0 || !ok) continue;
-          if (jd == 0) {   // h codes of tile t, written by both CTAs' epilogues
-            ok = mbar_wait(&bar_hlocal, (uint32_t)(t & 1), p.wait_limit_ns, &s_abort, 0x0604);
-            if (kPair) ok = ok && mbar_wait_cluster(&bar_hpeer, (uint32_t)(t & 1), p.wait_limit_ns, &s_abort, 0x060C);
-            if (!ok) break;
-            tc_fence_after();
-          }
           if (!(ok = acquire())) break;
           const uint32_t d_tmem = tmem_base + (uint32_t)(acc.stage * 256);
           for (int kb = 0; kb < NKD; kb += Cfg::kDownSteps) {
@@ -314,17 +304,19 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             const uint32_t b_addr = ring_addr + (uint32_t)(r.stage * Cfg::kSlotBytes);
 #pragma unroll
             for (int j = 0; j < Cfg::kDownSteps; ++j)
-              i8_mma_step<CG>(d_tmem, h_addr + (uint32_t)((kb + j) * (kBM * 128)), b_addr + (uint32_t)(j * Cfg::kBBytes),
-                              IDESC, kb + j == 0);
+              i8_mma_step<CG>(lead, d_tmem, h_addr + (uint32_t)((kb + j) * (kBM * 128)),
+                              b_addr + (uint32_t)(j * Cfg::kBBytes), IDESC, kb + j == 0);
             release_stage();
           }
           if (ok) publish();
         }
       }
-      if (kPair) tc_commit_pair(&bar_final);
-      else tc_commit(&bar_final);
-      volatile int dummy = 0;
-      mbar_wait(&bar_final, 0, p.wait_limit_ns, &dummy, 0x0606);
+      if (lane == 0) {
+        if (kPair) tc_commit_pair(&bar_final);
+        else tc_commit(&bar_final);
+        volatile int dummy = 0;
+        mbar_wait(&bar_final, 0, p.wait_limit_ns, &dummy, 0x0606);
+      }
     }
     // The other CTA of a pair passes its epilogue's "h ready" on to the leader.  A release at cluster scope took each
     // epilogue warp about 3500 cycles a tile while stores were under way; here nothing waits for it but the MMAs.
@@ -393,48 +385,48 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       fetch(i + 1);
       uint32_t hv[NGU][16];                  // h of tile i, bf16 pairs: 32 columns per job
       uint32_t top = 0;                      // maximum of |h| as bf16 bits, per half word
-      for (int jd = 0; jd < nd; ++jd) {
 #pragma unroll
-        for (int job = 0; job < NGU; ++job) {
-          if (i == mine || job * nd / NGU != jd || !ok || !(ok = job_ready())) continue;
-          const float* scl = &s_scale[(int)(n_job % kI8ScaleBufs)][32 * part];
-          const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(slot * 256 + 32 * part);
-          if (nv == 0) {
-            arrive(&bar_tempty[slot]);
-            job_done();
-            continue;
-          }
-          uint32_t v[2][16], u[2][16];
-          tmem_ld16(t_row, v[0]);
-          tmem_ld16(t_row + 128, u[0]);
-#pragma unroll
-          for (int c0 = 0; c0 < 32; c0 += 16) {
-            tmem_ld_wait();
-            if (c0 == 0) {
-              tmem_ld16(t_row + 16, v[1]);
-              tmem_ld16(t_row + 144, u[1]);
-            } else {
-              tc_fence_before();
-              arrive(&bar_tempty[slot]);
-            }
-            const uint32_t* vc = v[c0 / 16];
-            const uint32_t* uc = u[c0 / 16];
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 sg = *reinterpret_cast<const float4*>(scl + c0 + j);
-              const float4 su = *reinterpret_cast<const float4*>(scl + 128 + c0 + j);
-              const float2 f0 = i8_glu2<MODE>(i8_scaled(vc[j], vc[j + 1], sx, sg.x, sg.y),
-                                              i8_scaled(uc[j], uc[j + 1], sx, su.x, su.y));
-              const float2 f1 = i8_glu2<MODE>(i8_scaled(vc[j + 2], vc[j + 3], sx, sg.z, sg.w),
-                                              i8_scaled(uc[j + 2], uc[j + 3], sx, su.z, su.w));
-              const uint32_t p0 = pack_bf16x2(f0.x, f0.y), p1 = pack_bf16x2(f1.x, f1.y);
-              hv[job][(c0 + j) / 2] = p0;
-              hv[job][(c0 + j) / 2 + 1] = p1;
-              top = __vmaxu2(top, __vmaxu2(p0 & 0x7FFF7FFFu, p1 & 0x7FFF7FFFu));
-            }
-          }
+      for (int job = 0; job < NGU; ++job) {
+        if (i == mine || !ok || !(ok = job_ready())) continue;
+        const float* scl = &s_scale[(int)(n_job % kI8ScaleBufs)][32 * part];
+        const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(slot * 256 + 32 * part);
+        if (nv == 0) {
+          arrive(&bar_tempty[slot]);
           job_done();
+          continue;
         }
+        uint32_t v[2][16], u[2][16];
+        tmem_ld16(t_row, v[0]);
+        tmem_ld16(t_row + 128, u[0]);
+#pragma unroll
+        for (int c0 = 0; c0 < 32; c0 += 16) {
+          tmem_ld_wait();
+          if (c0 == 0) {
+            tmem_ld16(t_row + 16, v[1]);
+            tmem_ld16(t_row + 144, u[1]);
+          } else {
+            tc_fence_before();
+            arrive(&bar_tempty[slot]);
+          }
+          const uint32_t* vc = v[c0 / 16];
+          const uint32_t* uc = u[c0 / 16];
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 sg = *reinterpret_cast<const float4*>(scl + c0 + j);
+            const float4 su = *reinterpret_cast<const float4*>(scl + 128 + c0 + j);
+            const float2 f0 = i8_glu2<MODE>(i8_scaled(vc[j], vc[j + 1], sx, sg.x, sg.y),
+                                            i8_scaled(uc[j], uc[j + 1], sx, su.x, su.y));
+            const float2 f1 = i8_glu2<MODE>(i8_scaled(vc[j + 2], vc[j + 3], sx, sg.z, sg.w),
+                                            i8_scaled(uc[j + 2], uc[j + 3], sx, su.z, su.w));
+            const uint32_t p0 = pack_bf16x2(f0.x, f0.y), p1 = pack_bf16x2(f1.x, f1.y);
+            hv[job][(c0 + j) / 2] = p0;
+            hv[job][(c0 + j) / 2 + 1] = p1;
+            top = __vmaxu2(top, __vmaxu2(p0 & 0x7FFF7FFFu, p1 & 0x7FFF7FFFu));
+          }
+        }
+        job_done();
+      }
+      for (int jd = 0; jd < nd; ++jd) {
         if (i == 0 || !ok || !(ok = job_ready())) continue;
         const int cols = p.N - 256 * jd - 64 * part;   // a multiple of 16, may be <= 0
         const float* scl = &s_scale[(int)(n_job % kI8ScaleBufs)][64 * part];

@@ -68,33 +68,64 @@ __host__ __device__ constexpr uint32_t idesc_i8_s32(int M, int N) {
          | ((uint32_t)(M >> 4) << 24);   // M / 16
 }
 
+// D[tmem] (+)= A[smem] * B[smem]^T by the lane with `lead` set.  The whole warp runs the code around it: descriptors
+// and loop counters then stay in uniform registers, where tcgen05.mma takes them, which a branch on the lane prevents.
 template <int CG>
-__device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_i8(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
   if (CG == 2)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }
 
+// Arrive on the mbarrier (of both CTAs of a pair) when the lead lane's MMAs so far complete.
+template <int CG>
+__device__ __forceinline__ void tc_commit_i8(uint32_t lead, uint64_t* bar) {
+  if (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)0x3), "r"(lead)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+
+// mbar_wait by the whole warp; the same answer in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort,
+                                               unsigned int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns, abort, site)) != 0;
+}
+
+// Warp index in a uniform register.
+__device__ __forceinline__ int warp_id_uniform() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
+
 // One k-step: four MMAs of K = 32 over the 128-byte rows at the two shared addresses (1024-byte aligned).
 template <int CG>
-__device__ __forceinline__ void i8_mma_step(uint32_t d_tmem, uint32_t a_addr, uint32_t b_addr, uint32_t idesc,
+__device__ __forceinline__ void i8_mma_step(uint32_t lead, uint32_t d_tmem, uint32_t a_addr, uint32_t b_addr, uint32_t idesc,
                                             bool first) {
   const uint64_t a = smem_desc_k128(a_addr), b = smem_desc_k128(b_addr);   // + 2: 32 bytes on
-  tc_mma_i8<CG>(d_tmem, a, b, idesc, first ? 0u : 1u);
+  tc_mma_i8<CG>(lead, d_tmem, a, b, idesc, first ? 0u : 1u);
 #pragma unroll
-  for (int kk = 1; kk < kI8BK / 32; ++kk) tc_mma_i8<CG>(d_tmem, a + 2 * kk, b + 2 * kk, idesc, 1u);
+  for (int kk = 1; kk < kI8BK / 32; ++kk) tc_mma_i8<CG>(lead, d_tmem, a + 2 * kk, b + 2 * kk, idesc, 1u);
 }
 
 // Position in a ring of S stages: index, phase parity.
@@ -246,7 +277,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   __shared__ __align__(16) float s_scale[kI8ScaleBufs][BN];
   __shared__ __align__(8) uint64_t bar_sfull[kI8ScaleBufs], bar_sempty[kI8ScaleBufs];
 
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = warp_id_uniform(), lane = lane_id();
   const int crank = kPair ? (int)cluster_ctarank() : 0;   // 0 = leader of the pair
   const int unit = kPair ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
   const int n_units = kPair ? (int)(gridDim.x >> 1) : (int)gridDim.x;
@@ -388,34 +419,34 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
-    if (lane == 0 && crank == 0) {
+    if (crank == 0) {
       RingPos<S> r;
       RingPos<2> acc;
       bool ok = true;
-      const uint32_t base = smem_u32(smem);
-      for (long long tile = unit; tile < total && ok && !s_abort; tile += n_units) {
-        if (!mbar_wait(&bar_tempty[acc.stage], acc.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0503)) break;
+      const uint32_t lead = lane == 0, base = smem_u32(smem);
+      for (long long tile = unit; tile < total && ok; tile += n_units) {
+        if (!mbar_wait_warp(&bar_tempty[acc.stage], acc.phase ^ 1u, p.wait_limit_ns, &s_abort, 0x0503)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc.stage * BN);
         for (int kb = 0; kb < nk; ++kb) {
-          if (!(ok = mbar_wait(&bar_full[r.stage], r.phase, p.wait_limit_ns, &s_abort, 0x0504))) break;
+          if (!(ok = mbar_wait_warp(&bar_full[r.stage], r.phase, p.wait_limit_ns, &s_abort, 0x0504))) break;
           tc_fence_after();
           const uint32_t a_addr = base + (uint32_t)(r.stage * Cfg::kStageBytes);
-          i8_mma_step<CG>(d_tmem, a_addr, a_addr + Cfg::kABytes, IDESC, kb == 0);
-          if (kPair) tc_commit_pair_mc(&bar_empty[r.stage], 0x3);
-          else tc_commit(&bar_empty[r.stage]);
+          i8_mma_step<CG>(lead, d_tmem, a_addr, a_addr + Cfg::kABytes, IDESC, kb == 0);
+          tc_commit_i8<CG>(lead, &bar_empty[r.stage]);
           r.next();
         }
         if (!ok) break;
-        if (kPair) tc_commit_pair_mc(&bar_tfull[acc.stage], 0x3);
-        else tc_commit(&bar_tfull[acc.stage]);
+        tc_commit_i8<CG>(lead, &bar_tfull[acc.stage]);
         acc.next();
       }
       // all issued MMAs complete before TMEM is released
-      if (kPair) tc_commit_pair(&bar_final);
-      else tc_commit(&bar_final);
-      volatile int dummy = 0;
-      mbar_wait(&bar_final, 0, p.wait_limit_ns, &dummy, 0x0505);
+      if (lane == 0) {
+        if (kPair) tc_commit_pair(&bar_final);
+        else tc_commit(&bar_final);
+        volatile int dummy = 0;
+        mbar_wait(&bar_final, 0, p.wait_limit_ns, &dummy, 0x0505);
+      }
     }
     __syncwarp();
   } else if (warp >= 4 && warp < 4 + 4 * PARTS) {
