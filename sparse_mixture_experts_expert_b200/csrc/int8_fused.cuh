@@ -16,7 +16,7 @@
 // Jobs alternate between two TMEM accumulators of 256 columns, so an epilogue overlaps the next job's MMAs.  The codes
 // of tile i + 1 replace those of tile i after the epilogue has seen tile i's last down accumulator, that is after every
 // MMA that reads them.  The epilogue is what the kernel waits for, so it is kept lean: channel scales come by bulk
-// copies of the producer, y leaves through shared memory by TMA (a warp's 32 rows x 64 columns at a time; stores from
+// copies of the producer, y leaves through shared memory by TMA (a warp's 32 rows x 32 columns at a time; stores from
 // registers touch 32 lines each and held up the fence before the codes are published), and warps without rows skip
 // the arithmetic.  Roles as k_int8_gemm: warps 0, 2, 3 copies, warp 1 MMA,
 // warps 4-19 epilogue.
@@ -33,7 +33,7 @@ struct I8FusedCfg {
   static constexpr int kBBytes = (CG == 2 ? 128 : 256) * kI8BK;      // a 256-row B box, half of it per CTA of a pair
   static constexpr int kSlotBytes = kABytes + kBBytes;
   static constexpr int kDownSteps = CG == 2 ? H / 128 : 1;           // down k-steps whose B boxes share a slot
-  static constexpr int kOutBytes = CG == 2 ? kI8EpiWarps * 32 * 128 : 0;   // y staging: 4 KB per epilogue warp
+  static constexpr int kOutBytes = CG == 2 ? kI8EpiWarps * 32 * 64 : 0;    // y staging: 2 KB per epilogue warp
   static constexpr int kBudget = 208 * 1024 - 1024 - kHBytes - kOutBytes;
   static constexpr int kStages = kBudget / kSlotBytes > 8 ? 8 : kBudget / kSlotBytes;
   static constexpr size_t kSmemBytes = 1024 + (size_t)kHBytes + kOutBytes + (size_t)kStages * kSlotBytes;
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // h codes [128 columns][128 rows][128 B], y staging [16 warps][32 rows][128 B] (both swizzled), ring
+  // h codes [128 columns][128 rows][128 B], y staging [16 warps][32 rows][64 B] (both swizzled), ring
   uint8_t* stage_y = smem + Cfg::kHBytes;
   uint8_t* ring = stage_y + Cfg::kOutBytes;
   __shared__ __align__(8) uint64_t bar_full[S], bar_empty[S], bar_tfull[2], bar_tempty[2], bar_final;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       if (row < left_n - crank * kBM) sx_n = p.a_scale[(long long)row0_n + row];
     };
     fetch(0);
-    uint8_t* my_y = stage_y + ew * (32 * 128);
+    uint8_t* my_y = stage_y + ew * (32 * 64);
     uint8_t* h_row = smem + (size_t)row * 128;
     const uint32_t sw = (uint32_t)(row & 7);
     int nv = 0;                              // rows of this warp in tile i
@@ -437,10 +437,6 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           continue;
         }
         const bool by_tma = kPair && nv_d == 32;       // a warp whose rows all belong to the group
-        if (by_tma) {
-          if (lane == 0) bulk_wait_read();             // the last store has left the staging rows
-          __syncwarp();
-        }
         uint32_t v[2][16];
         tmem_ld16(t_row, v[0]);
 #pragma unroll
@@ -462,20 +458,25 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             o[j / 2] = pack_bf16x2(f0.x, f0.y);
             o[j / 2 + 1] = pack_bf16x2(f1.x, f1.y);
           }
-          if (by_tma) {   // staging row = lane, 16-byte chunk c at c ^ (lane & 7)
-            uint4* r = reinterpret_cast<uint4*>(my_y + lane * 128);
-            r[(uint32_t)(c0 / 8) ^ (uint32_t)(lane & 7)] = make_uint4(o[0], o[1], o[2], o[3]);
-            r[(uint32_t)(c0 / 8 + 1) ^ (uint32_t)(lane & 7)] = make_uint4(o[4], o[5], o[6], o[7]);
+          if (by_tma) {   // 32 columns at a time: staging row = lane, 16-byte chunk c at c ^ ((lane >> 1) & 3)
+            if (c0 % 32 == 0) {
+              if (lane == 0) bulk_wait_read();         // the last store has left the staging rows
+              __syncwarp();
+            }
+            uint4* r = reinterpret_cast<uint4*>(my_y + lane * 64);
+            const uint32_t c = (c0 / 8) & 3, x = (uint32_t)(lane >> 1) & 3u;
+            r[c ^ x] = make_uint4(o[0], o[1], o[2], o[3]);
+            r[(c + 1) ^ x] = make_uint4(o[4], o[5], o[6], o[7]);
+            if (c0 % 32 == 16) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&tmY, my_y, 256 * jd + 64 * part + c0 - 16, (int)y_row0);
+                bulk_commit();
+              }
+            }
           } else if (lane < nv_d && c0 < cols) {
             st_row16(p.out + (y_row0 + lane) * p.N + 256 * jd + 64 * part + c0, o, wide);
-          }
-        }
-        if (by_tma) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&tmY, my_y, 256 * jd + 64 * part, (int)y_row0);
-            bulk_commit();
           }
         }
         job_done();

@@ -243,17 +243,18 @@ static EncodeTiledFn get_encoder() {
   return fn;
 }
 
-// bf16 tensor [outer..., rows, K] (K innermost), box = 64 x box_rows (x 1).
-static int make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, int box_rows) {
+// bf16 tensor [outer..., rows, K] (K innermost), box = 64 (or box_cols) x box_rows (x 1).
+static int make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, int box_rows,
+                    int box_cols = kBK, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn enc = get_encoder();
   if (!enc) return MOE_CUDA_ERROR;
   cuuint64_t strides[2];
   strides[0] = dims[0] * 2;
   if (rank == 3) strides[1] = dims[0] * dims[1] * 2;
-  cuuint32_t box[3] = {(cuuint32_t)kBK, (cuuint32_t)box_rows, 1};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MOE_OK : MOE_CUDA_ERROR;
 }
@@ -830,7 +831,7 @@ static int launch_i8_fused_t(const I8Params& p, const void* xq, const void* w13,
   if (rc) return rc;
   CUtensorMap ty;
   const cuuint64_t dy[2] = {(cuuint64_t)p.N, (cuuint64_t)p.R};
-  rc = make_map(&ty, p.out, 2, dy, 32);
+  rc = make_map(&ty, p.out, 2, dy, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (rc) return rc;
   const long long TM = (long long)kBM * CG;
   const long long tiles = p.group_rows ? (p.R / TM + p.n_groups) : cdiv(p.R, TM);
