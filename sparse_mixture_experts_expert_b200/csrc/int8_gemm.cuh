@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 
 // Codes and scales of the rows that the groups hold (h between the two products); rows outside every group are not
 // read.  A row per TPR threads, the filled rows dealt over a fixed grid.
-template <int TPR>
+template <int TPR, int NV>
 __global__ void __launch_bounds__(256) k_quant_groups(const __nv_bfloat16* __restrict__ x, const I8Params p,
                                                       int8_t* __restrict__ q, float* __restrict__ scale) {
   pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(256) k_quant_groups(const __nv_bfloat16* __res
     const int i = (int)(on ? i0 + sub : i0);
     const int g = i8_find_group(s_prefix, p.n_groups, i);
     const size_t r = (size_t)(s_gstart[g] + i - s_prefix[g]);
-    const float s = quant_row<TPR>(x + r * K, K, on, s_max, [&](int c, uint2 v) {
+    const float s = quant_row<TPR, NV>(x + r * K, K, on, s_max, [&](int c, uint2 v) {
       reinterpret_cast<uint2*>(q + r * K)[c] = v;
     });
     if (on && (int)threadIdx.x % TPR == 0) scale[r] = s;

@@ -17,7 +17,7 @@
 namespace moe {
 
 constexpr float kQuantTiny = 1.5046327690525280e-36f;   // 2^-119
-constexpr int kQuantVec = 4;                             // 8-element vectors a thread keeps between the two passes
+constexpr int kQuantVec = 4;   // 8-element vectors a thread keeps between the two passes, unless more are asked for
 
 // Eight elements as they lie in memory.
 template <typename T> struct RawVec;
@@ -78,20 +78,20 @@ __device__ __forceinline__ uint2 quant_vec(const RawVec<T>& v, float r) {
 
 // One row by TPR threads (8 or 32 lanes of a warp, or the CTA's 256): maximum, then codes handed to put(vector index,
 // 8 codes); returns the scale.  Every thread of the warp (or CTA) takes part; with on == false it reads and puts
-// nothing.  Rows longer than TPR * kQuantVec vectors are read a second time past that.
-template <int TPR, typename T, typename Put>
+// nothing.  Rows longer than TPR * NV vectors are read a second time past that.
+template <int TPR, int NV, typename T, typename Put>
 __device__ __forceinline__ float quant_row(const T* __restrict__ x, int K, bool on, uint32_t* s_max, Put put) {
   const int nvec = on ? K >> 3 : 0;
   const int th = (int)threadIdx.x % TPR;
-  RawVec<T> v[kQuantVec];
+  RawVec<T> v[NV];
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kQuantVec; ++i)
+  for (int i = 0; i < NV; ++i)
     if (th + i * TPR < nvec) v[i].load(x + 8 * (th + i * TPR));
 #pragma unroll
-  for (int i = 0; i < kQuantVec; ++i)
+  for (int i = 0; i < NV; ++i)
     if (th + i * TPR < nvec) m = max(m, v[i].top());
-  for (int c = th + kQuantVec * TPR; c < nvec; c += TPR) {
+  for (int c = th + NV * TPR; c < nvec; c += TPR) {
     RawVec<T> u;
     u.load(x + 8 * c);
     m = max(m, u.top());
@@ -113,9 +113,9 @@ __device__ __forceinline__ float quant_row(const T* __restrict__ x, int K, bool 
   float s, r;
   quant_scale(__uint_as_float(m), s, r);
 #pragma unroll
-  for (int i = 0; i < kQuantVec; ++i)
+  for (int i = 0; i < NV; ++i)
     if (th + i * TPR < nvec) put(th + i * TPR, quant_vec(v[i], r));
-  for (int c = th + kQuantVec * TPR; c < nvec; c += TPR) {
+  for (int c = th + NV * TPR; c < nvec; c += TPR) {
     RawVec<T> u;
     u.load(x + 8 * c);
     put(c, quant_vec(u, r));
@@ -124,14 +124,14 @@ __device__ __forceinline__ float quant_row(const T* __restrict__ x, int K, bool 
 }
 
 // Rows 0 .. rows-1 of x [rows, K], 256 / TPR rows per CTA.
-template <int TPR, typename T>
+template <int TPR, int NV, typename T>
 __global__ void __launch_bounds__(256) k_quant_rows(const T* __restrict__ x, long long rows, int K,
                                                     int8_t* __restrict__ q, float* __restrict__ scale) {
   pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
   __shared__ uint32_t s_max[8];
   const long long r = (long long)blockIdx.x * (256 / TPR) + (int)threadIdx.x / TPR;
   const bool on = r < rows;
-  const float s = quant_row<TPR>(x + r * K, K, on, s_max, [&](int c, uint2 v) {
+  const float s = quant_row<TPR, NV>(x + r * K, K, on, s_max, [&](int c, uint2 v) {
     reinterpret_cast<uint2*>(q + r * K)[c] = v;
   });
   if (on && (int)threadIdx.x % TPR == 0) scale[r] = s;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(256) k_quant_slots(const __nv_bfloat16* __rest
     p[j] = on && j < k ? slot_pos[t * k + j] : -1;
     if ((unsigned)p[j] >= (unsigned)R) p[j] = -1;
   }
-  const float s = quant_row<TPR>(x + t * d, d, on, s_max, [&](int c, uint2 v) {
+  const float s = quant_row<TPR, kQuantVec>(x + t * d, d, on, s_max, [&](int c, uint2 v) {
 #pragma unroll
     for (int j = 0; j < KMAX; ++j)
       if (p[j] >= 0) reinterpret_cast<uint2*>(q + (size_t)p[j] * d)[c] = v;

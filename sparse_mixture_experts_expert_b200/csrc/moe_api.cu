@@ -770,14 +770,28 @@ static int int8_gemm(int mode, const void* A, const float* a_scale, long long R,
 // has several loads in flight: 8 lanes up to 256 columns, a warp up to 1024, else the CTA.
 static int quant_threads(int K) { return K <= 8 * 8 * kQuantVec ? 8 : K <= 32 * 8 * kQuantVec ? 32 : 256; }
 
+// bf16 rows of 1024 to 4096 columns, where there are enough of them to fill the GPU with a warp each: 16 vectors a lane.
+// (16384 rows of 4096: QWARP us; a CTA a row, whose threads hold two vectors and meet at a barrier: 58 us.)
+static bool quant_warp_rows(int K, long long rows) {
+  return K > 32 * 8 * kQuantVec && K <= 32 * 8 * 16 && rows >= 32ll * num_sms();
+}
+
 // Codes and scales of x [rows, K].
 template <typename T>
 static int launch_quant_rows(const T* x, long long rows, int K, int8_t* q, float* scale, cudaStream_t st) {
-  const int tpr = quant_threads(K);
+  constexpr int V = kQuantVec;
+  const bool wide = sizeof(T) == 2 && quant_warp_rows(K, rows);
+  const int tpr = wide ? 32 : quant_threads(K);
   const unsigned blocks = (unsigned)cdiv(rows * tpr, 256);
-  if (tpr == 8) MOE_LAUNCH((k_quant_rows<8, T>), blocks, 256, 0, st, x, rows, K, q, scale);
-  else if (tpr == 32) MOE_LAUNCH((k_quant_rows<32, T>), blocks, 256, 0, st, x, rows, K, q, scale);
-  else MOE_LAUNCH((k_quant_rows<256, T>), blocks, 256, 0, st, x, rows, K, q, scale);
+  if (wide) {
+    if constexpr (sizeof(T) == 2) MOE_LAUNCH((k_quant_rows<32, 16, T>), blocks, 256, 0, st, x, rows, K, q, scale);
+  } else if (tpr == 8) {
+    MOE_LAUNCH((k_quant_rows<8, V, T>), blocks, 256, 0, st, x, rows, K, q, scale);
+  } else if (tpr == 32) {
+    MOE_LAUNCH((k_quant_rows<32, V, T>), blocks, 256, 0, st, x, rows, K, q, scale);
+  } else {
+    MOE_LAUNCH((k_quant_rows<256, V, T>), blocks, 256, 0, st, x, rows, K, q, scale);
+  }
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -903,12 +917,15 @@ static int int8_ffn(const moe_shape* s, int hidden, long long R, const void* xq,
     p.n_groups = n_groups;
     p.R = R;
     p.K = hidden;
-    const int tpr = quant_threads(hidden);
+    const bool wide = quant_warp_rows(hidden, R);
+    const int tpr = wide ? 32 : quant_threads(hidden);
     const long long most = 8ll * num_sms();   // 256-thread CTAs resident at once
     const unsigned blocks = (unsigned)std::min(most, cdiv(R * tpr, 256));
-    if (tpr == 8) MOE_LAUNCH((k_quant_groups<8>), blocks, 256, 0, st, hb, p, hc, hs);
-    else if (tpr == 32) MOE_LAUNCH((k_quant_groups<32>), blocks, 256, 0, st, hb, p, hc, hs);
-    else MOE_LAUNCH((k_quant_groups<256>), blocks, 256, 0, st, hb, p, hc, hs);
+    constexpr int V = kQuantVec;
+    if (wide) MOE_LAUNCH((k_quant_groups<32, 16>), blocks, 256, 0, st, hb, p, hc, hs);
+    else if (tpr == 8) MOE_LAUNCH((k_quant_groups<8, V>), blocks, 256, 0, st, hb, p, hc, hs);
+    else if (tpr == 32) MOE_LAUNCH((k_quant_groups<32, V>), blocks, 256, 0, st, hb, p, hc, hs);
+    else MOE_LAUNCH((k_quant_groups<256, V>), blocks, 256, 0, st, hb, p, hc, hs);
     MOE_LAUNCH_CHECK();
   }
   return int8_gemm(kModePlain, hq, hs, R, hidden, w2, s2, n_groups, s->d, 0, s->d, gstart, grows, y, st, pair);
