@@ -53,10 +53,11 @@ struct I8Cfg {
   static constexpr int kABytes = kBM * kI8BK;
   static constexpr int kBBytes = (CG == 2 ? BN / 2 : BN) * kI8BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kBudget = 211 * 1024 - 1024;
+  static constexpr int kOutBytes = CG == 2 ? kI8EpiWarps * 32 * 64 : 0;   // output staging: 2 KB per epilogue warp
+  static constexpr int kBudget = 211 * 1024 - 1024 - kOutBytes;
   static constexpr int kStages = kBudget / kStageBytes > 8 ? 8 : kBudget / kStageBytes;
   static constexpr int kTmemCols = 2 * BN;      // two accumulators (128, 256 or 512 columns)
-  static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes;
+  static constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kOutBytes;
 };
 
 // Instruction descriptor, kind::i8: D s32, A and B signed 8-bit, both K-major, M x N.
@@ -252,7 +253,7 @@ __device__ __forceinline__ int i8_find_group(const int* prefix, int G, int mt) {
 template <int MODE, int BN, int CG>
 __global__ void __launch_bounds__(kI8Threads, 1)
     k_int8_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAFew,
-                const __grid_constant__ CUtensorMap tmB, const I8Params p) {
+                const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmOut, const I8Params p) {
   pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
   using Cfg = I8Cfg<BN, CG>;
   constexpr bool kGLU = MODE == kModeSwiGLU || MODE == kModeGeGLU;
@@ -467,11 +468,13 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       sx = row < rows_left - crank * kBM ? p.a_scale[(long long)row0 + row] : 0.f;
     };
     fetch(unit);
+    uint8_t* stg = smem + (size_t)S * Cfg::kStageBytes + (kPair ? ew * (32 * 64) : 0);
     for (long long tile = unit; tile < total && !s_abort; tile += n_units, ++n_tile) {
-      const bool live = row < rows_left - crank * kBM;
+      const int nv = max(0, min(32, rows_left - crank * kBM - q * 32));   // rows of this warp
       const float sxc = sx;
-      __nv_bfloat16* out = p.out + ((long long)row0 + row) * p.N + n0 + c_base;
-      const int cols = p.N - n0 - c_base;   // N is a multiple of 16: whole chunks
+      const long long o_row0 = (long long)row0 + q * 32;
+      const int o_col0 = n0 + c_base;
+      const int cols = p.N - o_col0;        // N is a multiple of 16: whole chunks
       fetch(tile + n_units);
       const int sb = (int)(n_tile % kI8ScaleBufs);
       if (!mbar_wait(&bar_sfull[sb], (uint32_t)((n_tile / kI8ScaleBufs) & 1), p.wait_limit_ns, &s_abort, 0x0509)) break;
@@ -479,17 +482,25 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       if (!mbar_wait(&bar_tfull[acc], acc_phase, p.wait_limit_ns, &s_abort, 0x0506)) break;
       tc_fence_after();
       const uint32_t t_row = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN + c_base);
+      const bool some = nv > 0 && cols > 0;
+      // A warp whose 32 rows all belong to the group sends them out by TMA, 32 columns at a time, through 2 KB of shared
+      // memory (row = lane, 16-byte chunk c at c ^ ((lane >> 1) & 3)); else its lanes store their rows themselves.
+      const bool by_tma = kPair && nv == 32;
       // chunks of 16 columns; the next chunk's loads are in flight while one is worked on
       uint32_t v[2][16], u[2][kGLU ? 16 : 1];
-      tmem_ld16(t_row, v[0]);
-      if constexpr (kGLU) tmem_ld16(t_row + OUTN, u[0]);
+      if (some) {
+        tmem_ld16(t_row, v[0]);
+        if constexpr (kGLU) tmem_ld16(t_row + OUTN, u[0]);
+      }
 #pragma unroll
       for (int c0 = 0; c0 < CW; c0 += 16) {
         const int b = (c0 / 16) & 1;
-        tmem_ld_wait();
+        if (some) tmem_ld_wait();
         if (c0 + 16 < CW) {
-          tmem_ld16(t_row + c0 + 16, v[b ^ 1]);
-          if constexpr (kGLU) tmem_ld16(t_row + OUTN + c0 + 16, u[b ^ 1]);
+          if (some) {
+            tmem_ld16(t_row + c0 + 16, v[b ^ 1]);
+            if constexpr (kGLU) tmem_ld16(t_row + OUTN + c0 + 16, u[b ^ 1]);
+          }
         } else {   // the accumulator is drained: one arrival per epilogue warp (on the leader)
           tc_fence_before();
           __syncwarp();
@@ -498,6 +509,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             else mbar_arrive(&bar_tempty[acc]);
           }
         }
+        if (!some) continue;
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
@@ -512,12 +524,32 @@ __global__ void __launch_bounds__(kI8Threads, 1)
           o[i / 2] = pack_bf16x2(f0.x, f0.y);
           o[i / 2 + 1] = pack_bf16x2(f1.x, f1.y);
         }
-        if (live && c0 < cols) st_row16(out + c0, o, wide);
+        if (by_tma) {
+          if (c0 % 32 == 0) {
+            if (lane == 0) bulk_wait_read();   // the last store has left the staging rows
+            __syncwarp();
+          }
+          uint4* r = reinterpret_cast<uint4*>(stg + lane * 64);
+          const uint32_t c = (c0 / 8) & 3, x = (uint32_t)(lane >> 1) & 3u;
+          r[c ^ x] = make_uint4(o[0], o[1], o[2], o[3]);
+          r[(c + 1) ^ x] = make_uint4(o[4], o[5], o[6], o[7]);
+          if (c0 % 32 == 16) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tmOut, stg, o_col0 + c0 - 16, (int)o_row0);
+              bulk_commit();
+            }
+          }
+        } else if (lane < nv && c0 < cols) {
+          st_row16(p.out + (o_row0 + lane) * p.N + o_col0 + c0, o, wide);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_sempty[sb]);
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
+    if (kPair && lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   if (kPair) cluster_sync_all();  // neither CTA leaves while the pair's MMAs or arrivals may touch it

@@ -701,7 +701,7 @@ static int make_map_i8(CUtensorMap* m, const void* base, int rank, const cuuint6
 }
 
 template <int MODE, int BN, int CG>
-static int launch_i8_t(const CUtensorMap& ta, const CUtensorMap& taf, const CUtensorMap& tb, const I8Params& p, long long ub_mtiles,
+static int launch_i8_t(const CUtensorMap& ta, const CUtensorMap& taf, const CUtensorMap& tb, const CUtensorMap& to, const I8Params& p, long long ub_mtiles,
                        cudaStream_t st) {
   using Cfg = I8Cfg<BN, CG>;
   constexpr int OUTN = (MODE == kModeSwiGLU || MODE == kModeGeGLU) ? BN / 2 : BN;
@@ -715,7 +715,7 @@ static int launch_i8_t(const CUtensorMap& ta, const CUtensorMap& taf, const CUte
   const long long tiles = ub_mtiles * cdiv(p.N, OUTN);
   const int units = (int)std::max<long long>(1, std::min<long long>(num_sms() / CG, tiles));
   MOE_CUDA_TRY(launch_pdl(k_int8_gemm<MODE, BN, CG>, dim3((unsigned)(CG * units)), dim3(kI8Threads), Cfg::kSmemBytes,
-                          st, (unsigned)CG, ta, taf, tb, p));
+                          st, (unsigned)CG, ta, taf, tb, to, p));
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -737,6 +737,10 @@ static int int8_gemm(int mode, const void* A, const float* a_scale, long long R,
   if (rc) return rc;
   rc = make_map_i8(&tb, B, 3, db, (glu || pair) ? BN / 2 : BN);
   if (rc) return rc;
+  CUtensorMap to;
+  const cuuint64_t dout[2] = {(cuuint64_t)N, (cuuint64_t)R};
+  rc = make_map(&to, out, 2, dout, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (rc) return rc;
   I8Params p;
   p.group_start = gstart;
   p.group_rows = grows;
@@ -753,12 +757,12 @@ static int int8_gemm(int mode, const void* A, const float* a_scale, long long R,
   const long long TM = (long long)kBM * (pair ? 2 : 1);
   const long long ub = grows ? (R / TM + n_groups) : cdiv(R, TM);
   if (pair) {
-    if (mode == kModePlain) return launch_i8_t<kModePlain, 256, 2>(ta, taf, tb, p, ub, st);
-    if (mode == kModeSwiGLU) return launch_i8_t<kModeSwiGLU, 256, 2>(ta, taf, tb, p, ub, st);
-    return launch_i8_t<kModeGeGLU, 256, 2>(ta, taf, tb, p, ub, st);
+    if (mode == kModePlain) return launch_i8_t<kModePlain, 256, 2>(ta, taf, tb, to, p, ub, st);
+    if (mode == kModeSwiGLU) return launch_i8_t<kModeSwiGLU, 256, 2>(ta, taf, tb, to, p, ub, st);
+    return launch_i8_t<kModeGeGLU, 256, 2>(ta, taf, tb, to, p, ub, st);
   }
 #define MOE_I8_CASE(M_, BN_) \
-  if (mode == M_ && BN == BN_) return launch_i8_t<M_, BN_, 1>(ta, taf, tb, p, ub, st);
+  if (mode == M_ && BN == BN_) return launch_i8_t<M_, BN_, 1>(ta, taf, tb, to, p, ub, st);
   MOE_I8_CASE(kModePlain, 256) MOE_I8_CASE(kModePlain, 128) MOE_I8_CASE(kModePlain, 64)
   MOE_I8_CASE(kModeSwiGLU, 256) MOE_I8_CASE(kModeSwiGLU, 128) MOE_I8_CASE(kModeSwiGLU, 64)
   MOE_I8_CASE(kModeGeGLU, 256) MOE_I8_CASE(kModeGeGLU, 128) MOE_I8_CASE(kModeGeGLU, 64)
@@ -919,7 +923,7 @@ static int int8_ffn(const moe_shape* s, int hidden, long long R, const void* xq,
     p.K = hidden;
     const bool wide = quant_warp_rows(hidden, R);
     const int tpr = wide ? 32 : quant_threads(hidden);
-    const long long most = 8ll * num_sms();   // 256-thread CTAs resident at once
+    const long long most = (wide ? 2ll : 8ll) * num_sms();   // 256-thread CTAs resident at once
     const unsigned blocks = (unsigned)std::min(most, cdiv(R * tpr, 256));
     constexpr int V = kQuantVec;
     if (wide) MOE_LAUNCH((k_quant_groups<32, 16>), blocks, 256, 0, st, hb, p, hc, hs);
