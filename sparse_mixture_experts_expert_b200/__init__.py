@@ -493,26 +493,27 @@ def moe_quantize_int8(x, *, q=None, scales=None, stream=None):
     return q, scales
 
 
-def moe_permute_int8(shape: MoeShape, x, topk_idx, *, ws=None, stream=None):
-    """moe_permute with the rows quantised on the way: a dict with xq_perm [R, d] int8 and xs_perm [R] fp32 in the
-    place of x_perm.  With a capacity, the rows behind an expert's kept ones hold nothing in particular, and row_src
-    is -1 there."""
+def moe_permute_int8(shape: MoeShape, x, topk_idx, *, full=False, ws=None, stream=None):
+    """moe_permute with the rows quantised on the way: a dict with slot_pos, kept, offsets, xq_perm [R, d] int8 and
+    xs_perm [R] fp32; with ``full`` also drop_mask, counts and row_src (-1 in rows that no token fills).  With a
+    capacity, the rows behind an expert's kept ones hold nothing in particular."""
     T, d, E, k = shape.T, shape.d, shape.E, shape.k
     _want(x, torch.bfloat16, (T, d), "x")
     _want(topk_idx, torch.int32, (T, k), "topk_idx")
     dev, R = x.device, shape.R
     with _on(stream, x, topk_idx, ws):
         i32 = dict(dtype=torch.int32, device=dev)
-        out = dict(slot_pos=torch.empty(T, k, **i32), drop_mask=torch.empty(T, k, dtype=torch.uint8, device=dev),
-                   counts=torch.empty(E, **i32), kept=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32),
-                   row_src=torch.full((R,), -1, **i32) if shape.capacity > 0 else torch.empty(R, **i32),
+        out = dict(slot_pos=torch.empty(T, k, **i32), kept=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32),
                    xq_perm=torch.empty(R, d, dtype=torch.int8, device=dev),
                    xs_perm=torch.empty(R, dtype=torch.float32, device=dev))
+        if full:
+            out.update(drop_mask=torch.empty(T, k, dtype=torch.uint8, device=dev), counts=torch.empty(E, **i32),
+                       row_src=torch.full((R,), -1, **i32))
         if ws is None:
             ws = torch.empty(moe_workspace_size(shape), dtype=torch.uint8, device=dev)
         rc = _L().moe_permute_int8(ctypes.byref(shape), _ptr(x), _ptr(topk_idx), _ptr(out["slot_pos"]),
-                                   _ptr(out["drop_mask"]), _ptr(out["counts"]), _ptr(out["kept"]),
-                                   _ptr(out["offsets"]), _ptr(out["row_src"]), _ptr(out["xq_perm"]),
+                                   _ptr(out.get("drop_mask")), _ptr(out.get("counts")), _ptr(out["kept"]),
+                                   _ptr(out["offsets"]), _ptr(out.get("row_src")), _ptr(out["xq_perm"]),
                                    _ptr(out["xs_perm"]), _ptr(ws), ws.numel(), _stream())
         _check(rc, "moe_permute_int8")
     return out

@@ -46,7 +46,6 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     k_int8_fused(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXFew,
                  const __grid_constant__ CUtensorMap tmW13, const __grid_constant__ CUtensorMap tmW2,
                  const __grid_constant__ CUtensorMap tmY, const I8Params p, const float* __restrict__ s2) {
-  pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
   using Cfg = I8FusedCfg<H, CG>;
   static_assert(H == 128 || H == 256, "fused expert hidden width");
   constexpr bool kPair = CG == 2;
@@ -82,7 +81,6 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int nd = (p.N + 255) / 256;                 // down jobs per tile
   const int G = p.group_rows == nullptr ? 1 : p.n_groups;
 
-  if (warp == 3) i8_group_table(p, TM, s_prefix, s_gstart, s_grows);
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(&bar_full[s], 1); mbar_init(&bar_empty[s], 1); }
     for (int a = 0; a < 2; ++a) {
@@ -110,6 +108,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       tmem_relinquish();
     }
   }
+  pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
+  if (warp == 3) i8_group_table(p, TM, s_prefix, s_gstart, s_grows);
   tc_fence_before();
   if (kPair) cluster_sync_all();
   else __syncthreads();

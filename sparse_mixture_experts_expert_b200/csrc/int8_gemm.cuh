@@ -254,7 +254,6 @@ template <int MODE, int BN, int CG>
 __global__ void __launch_bounds__(kI8Threads, 1)
     k_int8_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAFew,
                 const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmOut, const I8Params p) {
-  pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
   using Cfg = I8Cfg<BN, CG>;
   constexpr bool kGLU = MODE == kModeSwiGLU || MODE == kModeGeGLU;
   constexpr bool kPair = CG == 2;
@@ -286,7 +285,6 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   const int nk = (p.K + kI8BK - 1) / kI8BK;
   const int G = p.group_rows == nullptr ? 1 : p.n_groups;
 
-  if (warp == 3) i8_group_table(p, TM, s_prefix, s_gstart, s_grows);
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < S; ++s) { mbar_init(&bar_full[s], 1); mbar_init(&bar_empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&bar_tfull[a], 1); mbar_init(&bar_tempty[a], CG * 4 * PARTS); }
@@ -307,6 +305,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       tmem_relinquish();
     }
   }
+  pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
+  if (warp == 3) i8_group_table(p, TM, s_prefix, s_gstart, s_grows);
   tc_fence_before();
   if (kPair) cluster_sync_all();  // both CTAs' barriers initialised before any cross-CTA arrival
   else __syncthreads();

@@ -168,4 +168,94 @@ __global__ void __launch_bounds__(256) k_quant_slots(const __nv_bfloat16* __rest
   }
 }
 
+// The whole of moe_permute_int8 for few (token, slot) pairs in one launch: counting, grouping and quantising.  Every CTA
+// counts all T k pairs itself (shared-memory additions of ones: the sums do not depend on their order), the pairs of
+// earlier CTAs' tokens apart, which gives its own tokens' first ranks without a pass over the GPU before; the ranks
+// among its own 256 / TPR tokens come from comparing their pairs.  Then its tokens are quantised into their rows.  The
+// results are those of k_chunk_hist, k_chunk_scan, k_scatter and k_quant_slots.
+constexpr int kSmallPairs = 2048;
+
+template <int TPR, int KMAX>
+__global__ void __launch_bounds__(256) k_permute_quant_small(const __nv_bfloat16* __restrict__ x,
+                                                             const int32_t* __restrict__ topk_idx, int T, int d, int E,
+                                                             int k, int cap, int32_t* __restrict__ slot_pos,
+                                                             uint8_t* __restrict__ drop, int32_t* __restrict__ counts,
+                                                             int32_t* __restrict__ kept, int32_t* __restrict__ offsets,
+                                                             int32_t* __restrict__ row_src, int8_t* __restrict__ q,
+                                                             float* __restrict__ scale) {
+  pdl_wait();  // inputs written by the previous kernel on the stream are visible past this point
+  constexpr int TOK = 256 / TPR;
+  __shared__ int s_cnt[512], s_before[512], s_off[513];
+  __shared__ int s_exp[TOK * KMAX], s_slot[TOK * KMAX];
+  __shared__ uint32_t s_max[8];
+  const int tid = threadIdx.x, t0 = blockIdx.x * TOK;
+  for (int e = tid; e < E; e += 256) s_cnt[e] = s_before[e] = 0;
+  __syncthreads();
+  for (int i = tid; i < T * k; i += 256) {
+    const int e = topk_idx[i];
+    if ((unsigned)e >= (unsigned)E) continue;
+    atomicAdd(&s_cnt[e], 1);
+    if (i < t0 * k) atomicAdd(&s_before[e], 1);
+  }
+  const int mine = min(TOK, T - t0) * k;   // this CTA's pairs
+  for (int i = tid; i < mine; i += 256) s_exp[i] = topk_idx[t0 * k + i];
+  __syncthreads();
+  if (tid < 32) {   // first row of each group
+    const int per = (E + 31) / 32, e0 = min(E, tid * per), e1 = min(E, e0 + per);
+    int local = 0;
+    for (int e = e0; e < e1; ++e) local += cap > 0 ? cap : s_cnt[e];
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (tid >= o) incl += v;
+    }
+    int run = incl - local;
+    for (int e = e0; e < e1; ++e) {
+      s_off[e] = run;
+      run += cap > 0 ? cap : s_cnt[e];
+    }
+    if (tid == 31) s_off[E] = incl;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int e = tid; e < E; e += 256) {
+      if (counts) counts[e] = s_cnt[e];
+      kept[e] = cap > 0 ? min(cap, s_cnt[e]) : s_cnt[e];
+      offsets[e] = s_off[e];
+    }
+    if (tid == 0) offsets[E] = s_off[E];
+  }
+  for (int i = tid; i < mine; i += 256) {
+    const int e = s_exp[i];
+    int pos = -1;
+    if ((unsigned)e < (unsigned)E) {
+      int rank = s_before[e];
+      for (int o = 0; o < i; ++o) rank += s_exp[o] == e;
+      if (cap == 0 || rank < cap) pos = s_off[e] + rank;
+    }
+    const int pair = t0 * k + i;
+    s_slot[i] = pos;
+    slot_pos[pair] = pos;
+    if (drop) drop[pair] = pos < 0 ? 1 : 0;
+    if (row_src && pos >= 0) row_src[pos] = pair;
+  }
+  __syncthreads();
+  const int lt = tid / TPR;
+  const bool on = t0 + lt < T;
+  int p[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) p[j] = on && j < k ? s_slot[lt * k + j] : -1;
+  const float s = quant_row<TPR, kQuantVec>(x + (size_t)(t0 + lt) * d, d, on, s_max, [&](int c, uint2 v) {
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+      if (p[j] >= 0) reinterpret_cast<uint2*>(q + (size_t)p[j] * d)[c] = v;
+  });
+  if (on && tid % TPR == 0) {
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+      if (p[j] >= 0) scale[p[j]] = s;
+  }
+}
+
 }  // namespace moe

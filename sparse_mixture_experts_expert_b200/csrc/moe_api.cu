@@ -874,6 +874,30 @@ static int launch_i8_fused(const moe_shape* s, int hidden, const I8Params& p, co
   return MOE_UNSUPPORTED_SHAPE;
 }
 
+// moe_permute_int8 in one launch, for at most kSmallPairs (token, slot) pairs.
+static int launch_permute_quant_small(const moe_shape* s, const void* x, const int32_t* idx, int32_t* slot,
+                                      uint8_t* drop, int32_t* counts, int32_t* kept, int32_t* offsets,
+                                      int32_t* row_src, int8_t* q, float* scale, cudaStream_t st) {
+  const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(x);
+  const int tpr = quant_threads(s->d);
+  const unsigned blocks = (unsigned)cdiv(s->T * (long long)tpr, 256);
+#define MOE_PSMALL_T(T_, N_)                                                                                       \
+  MOE_LAUNCH((k_permute_quant_small<T_, N_>), blocks, 256, 0, st, xb, idx, (int)s->T, s->d, s->E, s->k, s->capacity, \
+             slot, drop, counts, kept, offsets, row_src, q, scale)
+#define MOE_PSMALL(N_)                                                                                            \
+  if (s->k <= N_) {                                                                                               \
+    if (tpr == 8) MOE_PSMALL_T(8, N_);                                                                            \
+    else if (tpr == 32) MOE_PSMALL_T(32, N_);                                                                     \
+    else MOE_PSMALL_T(256, N_);                                                                                   \
+    MOE_LAUNCH_CHECK();                                                                                           \
+    return MOE_OK;                                                                                                \
+  }
+  MOE_PSMALL(2) MOE_PSMALL(8) MOE_PSMALL(16)
+#undef MOE_PSMALL
+#undef MOE_PSMALL_T
+  return MOE_UNSUPPORTED_SHAPE;
+}
+
 // One kernel for both products, or the products with h in memory between them.  The fused kernel gives a row tile to
 // one CTA (pair), which streams its expert's weights alone: right where the row tiles fill the GPU, and where an
 // expert is small enough that one SM streams it in the time that two more launches take.
@@ -1926,6 +1950,9 @@ int moe_permute_int8(const moe_shape* s, const void* x, const int32_t* topk_idx,
     return MOE_INVALID_ARGUMENT;
   const Workspace L = ws_layout(s);
   if (ws_bytes < L.total) return MOE_WORKSPACE_TOO_SMALL;
+  if (s->T * s->k <= kSmallPairs)
+    return launch_permute_quant_small(s, x, topk_idx, slot_pos, drop_mask, counts, kept, offsets, row_src, xq_perm,
+                                      xs_perm, stream);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   int32_t* cnt = reinterpret_cast<int32_t*>(ws + L.cnt);
   int32_t* cts = counts ? counts : reinterpret_cast<int32_t*>(ws + L.counts);

@@ -89,13 +89,17 @@ def test_leading_dimensions_and_given_outputs(lib):
 
 
 @pytest.mark.parametrize("T,E,k,d,cap,skew", [(1, 8, 2, 64, 0, 0.0), (300, 8, 2, 80, 0, 0.0), (1000, 192, 4, 768, 27, 1.2),
-                                              (70, 33, 5, 1040, 0, 1.0), (40, 16, 16, 16, 3, 0.0), (9, 48, 8, 7168, 0, 0.0)])
+                                              (70, 33, 5, 1040, 0, 1.0), (40, 16, 16, 16, 3, 0.0), (9, 48, 8, 7168, 0, 0.0),
+                                              # either side of the one-launch form's 2048 pairs, its three widths
+                                              (2048, 512, 1, 64, 0, 0.5), (2049, 512, 1, 64, 0, 0.5),
+                                              (128, 20, 16, 528, 30, 0.6), (129, 20, 16, 528, 30, 0.6),
+                                              (100, 7, 5, 1056, 0, 0.0), (256, 384, 8, 256, 2, 1.0)])
 def test_permute_int8_matches_the_oracle(lib, T, E, k, d, cap, skew):
     moe = lib
     s = moe.MoeShape(T=T, d=d, E=E, k=k, H=16, capacity=cap, wfmt=moe.WFMT_INT8)
     idx = synth.draw_topk_idx(T, E, k, seed=T, skew=skew)
     x = torch.randn(T, d, generator=torch.Generator().manual_seed(T)).bfloat16()
-    r = moe.moe_permute_int8(s, x.to(DEV), idx.to(DEV))
+    r = moe.moe_permute_int8(s, x.to(DEV), idx.to(DEV), full=True)
     ref = O.permute(idx.numpy(), E, cap)
     for key in ("slot_pos", "kept", "offsets", "row_src", "counts"):
         assert (npi(r[key]) == ref[key]).all(), key
@@ -349,7 +353,7 @@ def test_layer_in_a_graph_and_on_another_stream(lib):
     assert torch.equal(out, want)
     # the steps on a stream of their own, scratch and outputs allocated for it
     idx = _forward(moe, s, dv, ws=ws)["topk_idx"]
-    a = moe.moe_permute_int8(s, dv["x"], idx)
+    a = moe.moe_permute_int8(s, dv["x"], idx, full=True)
     ya = moe.moe_expert_ffn_int8(s, a["xq_perm"], a["xs_perm"], dv["w13"], dv["s13"], dv["w2"], dv["s2"],
                                  group_start=a["offsets"], group_rows=a["kept"])
     side = torch.cuda.Stream()
