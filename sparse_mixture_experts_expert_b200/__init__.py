@@ -503,7 +503,7 @@ def moe_permute_int8(shape: MoeShape, x, topk_idx, *, full=False, ws=None, strea
     dev, R = x.device, shape.R
     with _on(stream, x, topk_idx, ws):
         i32 = dict(dtype=torch.int32, device=dev)
-        out = dict(slot_pos=torch.empty(T, k, **i32), kept=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32),
+        out = dict(slot_pos=torch.empty_like(topk_idx), kept=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32),
                    xq_perm=torch.empty(R, d, dtype=torch.int8, device=dev),
                    xs_perm=torch.empty(R, dtype=torch.float32, device=dev))
         if full:
@@ -563,8 +563,8 @@ def moe_combine_backward(shape: MoeShape, dout, y_perm, slot_pos, topk_w, *, kep
     if kept is not None:
         _want(kept, torch.int32, (shape.E,), "kept")
     with _on(stream, dout, y_perm, slot_pos, topk_w, kept):
-        dy = torch.empty(R, d, dtype=torch.bfloat16, device=dout.device)
-        dw = torch.empty(T, k, dtype=torch.float32, device=dout.device) if want_dw else None
+        dy = torch.empty_like(y_perm)
+        dw = torch.empty_like(topk_w) if want_dw else None
         rc = _L().moe_combine_backward(ctypes.byref(shape), _ptr(dout), _ptr(y_perm), _ptr(slot_pos), _ptr(topk_w),
                                        _ptr(kept) if shape.capacity > 0 else None, _ptr(dy), _ptr(dw), _stream())
         _check(rc, "moe_combine_backward")
