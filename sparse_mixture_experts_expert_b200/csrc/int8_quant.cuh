@@ -172,8 +172,9 @@ __global__ void __launch_bounds__(256) k_quant_slots(const __nv_bfloat16* __rest
 // counts all T k pairs itself (shared-memory additions of ones: the sums do not depend on their order), the pairs of
 // earlier CTAs' tokens apart, which gives its own tokens' first ranks without a pass over the GPU before; the ranks
 // among its own 256 / TPR tokens come from comparing their pairs.  Then its tokens are quantised into their rows.  The
-// results are those of k_chunk_hist, k_chunk_scan, k_scatter and k_quant_slots.
-constexpr int kSmallPairs = 2048;
+// results are those of k_chunk_hist, k_chunk_scan, k_scatter and k_quant_slots (four launches / one, us: 256 tokens,
+// top-2, width 64: 7.3 / 3.8; 1024 tokens, top-4, width 768: 9.8 / 5.0; 1024 tokens, top-8, width 7168: 21.5 / 21.0).
+constexpr int kSmallPairs = 4096;
 
 template <int TPR, int KMAX>
 __global__ void __launch_bounds__(256) k_permute_quant_small(const __nv_bfloat16* __restrict__ x,

@@ -774,10 +774,10 @@ static int int8_gemm(int mode, const void* A, const float* a_scale, long long R,
 // has several loads in flight: 8 lanes up to 256 columns, a warp up to 1024, else the CTA.
 static int quant_threads(int K) { return K <= 8 * 8 * kQuantVec ? 8 : K <= 32 * 8 * kQuantVec ? 32 : 256; }
 
-// bf16 rows of 1024 to 4096 columns, where there are enough of them to fill the GPU with a warp each: 16 vectors a lane.
-// (16384 rows of 4096: QWARP us; a CTA a row, whose threads hold two vectors and meet at a barrier: 58 us.)
+// bf16 rows of 1024 to 4096 columns: a warp each with 16 vectors a lane, where there are enough rows (4096 columns, a
+// CTA a row / a warp a row: 16384 rows 38 / 31 us, 2000 rows 5.0 / 4.2, 1000 rows 3.2 / 3.2, 100 rows 1.8 / 2.8).
 static bool quant_warp_rows(int K, long long rows) {
-  return K > 32 * 8 * kQuantVec && K <= 32 * 8 * 16 && rows >= 32ll * num_sms();
+  return K > 32 * 8 * kQuantVec && K <= 32 * 8 * 16 && rows >= 8ll * num_sms();
 }
 
 // Codes and scales of x [rows, K].
@@ -860,9 +860,14 @@ static int launch_i8_fused_t(const I8Params& p, const void* xq, const void* w13,
   return MOE_OK;
 }
 
+// CTA pairs as for the bf16 experts: on average at least 192 rows per group.
+static bool i8_fused_pair(const moe_shape* s, long long R, int n_groups) {
+  return !(s->flags & MOE_FLAG_SINGLE_CTA_GEMM) && R >= 192ll * n_groups;
+}
+
 static int launch_i8_fused(const moe_shape* s, int hidden, const I8Params& p, const void* xq, const void* w13,
                            const void* w2, const float* s2, cudaStream_t st) {
-  const bool pair = !(s->flags & MOE_FLAG_SINGLE_CTA_GEMM) && p.R >= 192ll * p.n_groups;
+  const bool pair = i8_fused_pair(s, p.R, p.n_groups);
   const bool geglu = s->act == MOE_ACT_GEGLU;
 #define MOE_I8_FUSED(M_, H_, CG_) \
   if ((M_ == kModeGeGLU) == geglu && hidden == H_ && (CG_ == 2) == pair) \
@@ -899,12 +904,19 @@ static int launch_permute_quant_small(const moe_shape* s, const void* x, const i
 }
 
 // One kernel for both products, or the products with h in memory between them.  The fused kernel gives a row tile to
-// one CTA (pair), which streams its expert's weights alone: right where the row tiles fill the GPU, and where an
-// expert is small enough that one SM streams it in the time that two more launches take.
+// one CTA (pair), which streams its expert's weights alone.  That pays where an expert is so small that it takes less
+// time than two more launches, or where row tiles occupy at least a quarter of the GPU and the down product is not too
+// wide for the tile's epilogue to keep up (8-bit expert weights up to 1 MB).  Measured, unfused / fused in us
+// (experts x rows each, width x hidden): 4 x 100, 256 x 128: 12.4 / 9.3; 30 x 10, 512 x 128: 14.1 / 10.8; 16 x 700,
+// 768 x 256: 27.7 / 20.0; 8 x 12000, 768 x 256: 98 / 78; 48 x 1000, 2048 x 128: 92 / 83.  And the other side:
+// 8 x 64, 768 x 256: 13.8 / 15.3; 1 x 4000, 768 x 256: 16.8 / 17.6; 8 x 1, 2048 x 128: 15.5 / 20.3; 48 x 400,
+// 2048 x 256: 63 / 69; 48 x 1000, 7168 x 256: 305 / 337.
 static bool use_i8_fused(const moe_shape* s, int hidden, long long R, int n_groups) {
   if (hidden != 128 && hidden != 256) return false;
   const long long expert_bytes = 3ll * s->d * hidden;
-  return expert_bytes <= (3ll << 19) || R >= 64ll * num_sms();
+  const int cg = i8_fused_pair(s, R, n_groups) ? 2 : 1;
+  const long long tiles = R / (kBM * cg) + n_groups;
+  return expert_bytes <= (1ll << 18) || (expert_bytes <= (1ll << 20) && 4 * tiles * cg >= num_sms());
 }
 
 // y = FFN of the codes xq (scales xs) over groups; h [R, hidden] bf16, hq [R, hidden] and hs [R] are scratch, not
@@ -2016,8 +2028,9 @@ int moe_combine_backward(const moe_shape* s, const void* dout, const void* y_per
   const __nv_bfloat16* y = reinterpret_cast<const __nv_bfloat16*>(y_perm);
   __nv_bfloat16* dy = reinterpret_cast<__nv_bfloat16*>(dy_perm);
   const int R = (int)grouped_rows(s);
-  // a CTA per token where a warp per token would leave SMs without work
-  const bool wide = s->T < 8ll * num_sms() && s->d > 256;
+  // A CTA per token where a warp per token would leave SMs without work (a warp / a CTA, us; width 768, top-4: 64 tokens
+  // 3.6 / 2.6, 1000 tokens 3.8 / 5.0; width 7168, top-8: 1 token 22 / 6.3, 1000 tokens 55 / 49, 2000 tokens 80 / 88).
+  const bool wide = s->d > 256 && s->T < (s->d >= 4096 ? 8ll : 4ll) * num_sms();
   const unsigned tok = (unsigned)(wide ? s->T : cdiv(s->T, 8));
   const unsigned pad = kept ? (unsigned)(s->E * cdiv(s->capacity, kPadRows)) : 0u;
 #define MOE_CBWD(N_)                                                                                              \

@@ -90,9 +90,9 @@ def test_leading_dimensions_and_given_outputs(lib):
 
 @pytest.mark.parametrize("T,E,k,d,cap,skew", [(1, 8, 2, 64, 0, 0.0), (300, 8, 2, 80, 0, 0.0), (1000, 192, 4, 768, 27, 1.2),
                                               (70, 33, 5, 1040, 0, 1.0), (40, 16, 16, 16, 3, 0.0), (9, 48, 8, 7168, 0, 0.0),
-                                              # either side of the one-launch form's 2048 pairs, its three widths
-                                              (2048, 512, 1, 64, 0, 0.5), (2049, 512, 1, 64, 0, 0.5),
-                                              (128, 20, 16, 528, 30, 0.6), (129, 20, 16, 528, 30, 0.6),
+                                              # either side of the one-launch form's 4096 pairs, its three widths
+                                              (4096, 512, 1, 64, 0, 0.5), (4097, 512, 1, 64, 0, 0.5),
+                                              (256, 20, 16, 528, 60, 0.6), (257, 20, 16, 528, 60, 0.6),
                                               (100, 7, 5, 1056, 0, 0.0), (256, 384, 8, 256, 2, 1.0)])
 def test_permute_int8_matches_the_oracle(lib, T, E, k, d, cap, skew):
     moe = lib
@@ -168,6 +168,7 @@ def _ffn_case(moe, d, H, act, rows, starts=None, R=None, seed=0, flags=0, check=
 # fused kernel; both activations
 @pytest.mark.parametrize("d,H,act,rows", [(16, 16, 0, [1]), (16, 16, 1, [0, 3, 0, 1]), (80, 48, 0, [5, 0, 128, 129]),
                                           (64, 128, 0, [70, 33, 0, 257]), (272, 256, 0, [300, 1, 31, 32, 33]),
+                                          (2064, 128, 0, [5, 200]), (784, 256, 1, [9] * 45),
                                           (768, 256, 0, [700, 512, 64, 0, 90]), (768, 128, 1, [400, 300]),
                                           (128, 1040, 1, [17, 140]), (1040, 80, 0, [1, 2, 0, 4]), (256, 2048, 1, [130, 260])])
 def test_expert_ffn_matches_the_oracle(lib, d, H, act, rows):
@@ -178,7 +179,7 @@ def test_expert_ffn_matches_the_oracle(lib, d, H, act, rows):
 # (hidden 128 and 256, one to three jobs of 256 output columns), the two kernels on both, ragged groups throughout
 @pytest.mark.parametrize("d,H,act,groups,rows,flags", [(272, 256, 0, 5, 9000, 0), (528, 128, 1, 4, 11000, 0),
                                                        (768, 256, 0, 3, 15000, 0), (48, 256, 1, 6, 7000, 1),
-                                                       (64, 128, 0, 500, 3, 0), (592, 256, 0, 400, 5, 0),
+                                                       (64, 128, 0, 500, 3, 0), (336, 256, 0, 400, 5, 0),
                                                        (64, 320, 0, 6, 7000, 0), (80, 192, 1, 450, 2, 0)])
 def test_several_tiles_per_cta(lib, d, H, act, groups, rows, flags):
     moe = lib
