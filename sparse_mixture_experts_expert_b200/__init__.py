@@ -333,6 +333,12 @@ def moe_expert_ffn(shape: MoeShape, x_grouped, w13, w2, *, hidden=None, group_st
 
 
 def moe_combine(shape: MoeShape, y_perm, slot_pos, topk_w, y_shared=None, *, out=None, stream=None):
+    T, d, k = shape.T, shape.d, shape.k
+    _want(y_perm, torch.bfloat16, (shape.R, d), "y_perm")
+    _want(slot_pos, torch.int32, (T, k), "slot_pos")
+    _want(topk_w, torch.float32, (T, k), "topk_w")
+    if y_shared is not None:
+        _want(y_shared, torch.bfloat16, (T, d), "y_shared")
     if out is None:
         out = torch.empty(shape.T, shape.d, dtype=torch.bfloat16, device=y_perm.device)
     rc = _L().moe_combine(ctypes.byref(shape), _ptr(y_perm), _ptr(slot_pos), _ptr(topk_w), _ptr(y_shared),
@@ -347,6 +353,16 @@ def moe_forward(shape: MoeShape, x, w_router, w13, w2, *, bias=None, s13=None, s
     ``side_stream`` (a torch.cuda.Stream) lets a bf16 shared expert overlap the routing and routed experts."""
     T, d, E, k = shape.T, shape.d, shape.E, shape.k
     _want(x, torch.bfloat16, (T, d), "x")
+    if shape.wfmt == WFMT_INT8:
+        for n, H, sfx, ts in ((E, shape.H, "", (w13, s13, w2, s2)),
+                              (1, shape.H_s, "_sh", (w13_sh, s13_sh, w2_sh, s2_sh))):
+            if H == 0:
+                continue
+            for t, name, dtype, dims in zip(ts, ("w13", "s13", "w2", "s2"), (torch.int8, torch.float32) * 2,
+                                            ((n, 2 * H, d), (n, 2 * H), (n, d, H), (n, d))):
+                if t is None:
+                    raise ValueError(f"{name}{sfx}: missing")
+                _want(t, dtype, dims, name + sfx)
     dev = x.device
     if out is None:
         out = torch.empty(T, d, dtype=torch.bfloat16, device=dev)

@@ -154,6 +154,33 @@ def test_binding_refuses_types_shapes_and_host_tensors():
         moe.moe_expert_ffn(q, z(8, 64), a["w13"], a["w2"], s13=a["s13"], s2=a["s2"], h=z(8, 16))
 
 
+def test_layer_and_combine_refuse_other_types_and_shapes():
+    s = _shape(T=4, E=2, H=16, H_s=32)
+    x, wr = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(2, 64)
+    a = dict(w13=torch.zeros(2, 32, 64, dtype=torch.int8), w2=torch.zeros(2, 64, 16, dtype=torch.int8),
+             s13=torch.zeros(2, 32), s2=torch.zeros(2, 64), w13_sh=torch.zeros(1, 64, 64, dtype=torch.int8),
+             s13_sh=torch.zeros(1, 64), w2_sh=torch.zeros(1, 64, 32, dtype=torch.int8), s2_sh=torch.zeros(1, 64))
+    call = lambda **kw: moe.moe_forward(s, x, wr, **{**a, **kw})
+    with pytest.raises(TypeError, match="s13"):
+        call(s13=a["s13"].bfloat16())           # half the bytes the kernels would read
+    with pytest.raises(TypeError, match="w13"):
+        call(w13=a["w13"].bfloat16())
+    with pytest.raises(ValueError, match="s2_sh"):
+        call(s2_sh=torch.zeros(1, 32))
+    with pytest.raises(ValueError, match="w2_sh: missing"):
+        call(w2_sh=None)
+    f = _shape(T=4, wfmt=0)
+    y, p, w = torch.zeros(8, 64, dtype=torch.bfloat16), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    with pytest.raises(TypeError, match="y_perm"):
+        moe.moe_combine(f, y.float(), p, w)
+    with pytest.raises(ValueError, match="y_perm"):
+        moe.moe_combine(f, y[:7], p, w)
+    with pytest.raises(TypeError, match="topk_w"):
+        moe.moe_combine(f, y, p, w.bfloat16())
+    with pytest.raises(ValueError, match="y_shared"):
+        moe.moe_combine(f, y, p, w, y)
+
+
 # ------------------------------------------------------------------ dispatch and combine with stand-ins
 
 
