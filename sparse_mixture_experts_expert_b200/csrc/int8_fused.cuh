@@ -18,8 +18,12 @@
 // MMA that reads them.  The epilogue is what the kernel waits for, so it is kept lean: channel scales come by bulk
 // copies of the producer, y leaves through shared memory by TMA (a warp's 32 rows x 32 columns at a time; stores from
 // registers touch 32 lines each and held up the fence before the codes are published), and warps without rows skip
-// the arithmetic.  Roles as k_int8_gemm: warps 0, 2, 3 copies, warp 1 MMA,
-// warps 4-19 epilogue.
+// the arithmetic.  Roles as k_int8_gemm: warps 0, 2, 3 copies, warp 1 MMA, warps 4-19 epilogue.
+//
+// Measured (B200), 131072 rows over 192 experts of 768 x 256: 98 us against 172 us for the three kernels (floors: 414 MB
+// 64 us, 155 GOP 47 us).  Tensor pipe 39% busy, issue slots 51%, DRAM 46%: the waits of the MMA thread are about
+// evenly on accumulators (the down epilogues), on operands and on its own issue.  Eight epilogue warps for each
+// accumulator instead of sixteen for one at a time took 5 us more, prefetching the next tile into L2 33 us more.
 #pragma once
 
 #include "int8_gemm.cuh"

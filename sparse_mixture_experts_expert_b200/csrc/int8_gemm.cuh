@@ -3,22 +3,29 @@
 //   out[rows of group g] = epilogue( A[rows of group g] . B_g^T ),   A [R, K] int8 codes, B_g int8 codes.
 // The integer sums are exact (|code| <= 128, K <= 65536: below 2^31); the epilogue forms float(sum) s_row s_col.
 //   gate/up (GLU): a tile holds the gate and the up slice of the same hidden columns side by side, and writes
-//     h = act(g) u rounded once to bf16 (the layer's h has that type for every weight format; the rounding is a
-//     tenth of the step of the 8-bit codes that h becomes next);
+//     h = act(g) u rounded once to bf16 (the layer's h has that type for every weight format, and it halves what the
+//     two kernels around h move; the rounding is at most half a step of the 8-bit codes that h becomes next, for the
+//     row's largest elements, and 2^-8 of the value for the others);
 //   down (plain): writes y in bf16.
 // ExpertMesh README (grouped routed-expert products of quantised weights in [expert, output, input] order).
 //
-// Structure as k_grouped_gemm: persistent CTAs, warps 0 and 2 feed A and B tiles of 128 bytes of K by TMA into a ring,
-// warp 3 the channel scales, warp 1 issues tcgen05.mma (M = 128, or 256 over a CTA pair; four MMAs of K = 32 per stage), and the epilogue drains
-// one accumulator while the next one fills.  A k-step holds twice the inputs of a bf16 one for the same bytes and the
-// same MMA time, so a tile's main loop takes half as long and the epilogue weighs twice as much: sixteen epilogue warps
-// (four per TMEM quarter, each on a quarter of the columns) instead of four, and rows stored straight from the
-// registers in whole 32-byte sectors instead of through shared memory.
+// Structure as k_grouped_gemm: persistent CTAs; warps 0 and 2 feed A and B tiles of 128 bytes of K by TMA into a ring,
+// warp 3 the channel scales; warp 1 issues tcgen05.mma (M = 128, or 256 over a CTA pair; four MMAs of K = 32 per
+// stage); the epilogue drains one accumulator while the next one fills.  A k-step holds twice the inputs of a bf16 one
+// for the same bytes and the same MMA time, so a tile's main loop takes half as long and the epilogue weighs twice as
+// much: sixteen epilogue warps (four per TMEM quarter, each on a quarter of the columns) instead of four, arithmetic
+// in packed fp32 pairs, and no access to global memory between a tile's MMAs and its stores.  Pair tiles store by TMA,
+// others straight from the registers in whole 32-byte sectors.
+// Measured (B200): one dense group of 8192 rows, 7168 -> 2 x 4096: 263 us, 3660 TOP/s.  16384 rows over 32 experts,
+// GeGLU 768 -> 4096: gate/up 108 us (1900 TOP/s; tensor pipe 52% busy, DRAM 36%), down 55 us (1870 TOP/s).  There the
+// groups cost the rest: a third of the 256-row tiles is nearly empty, and 300 MB of weights come from HBM (one dense
+// group of that shape: 74 and 40 us).  Keeping the A tile in shared memory for four column tiles (half the operand
+// bytes) left the gate/up kernel at 121 us against 118, and 128-row tiles on single CTAs at 109 against 108.
+// 64 rows over 48 experts of 7168 x 2048: 159 and 85 us, the weights at 6.4 TB/s.
 // Row tiles of at most 64 rows load them in boxes of 32, no more than the group has: with a handful of rows an expert
 // (decode) the weights are then nearly all that moves.  Shared memory behind those rows holds whatever it held; integer
 // products of it are finite and stay in rows that the epilogue does not store.  Fuller tiles take one box of 128 rows
-// (four of 32 made the gate/up kernel of 16384 rows, 768 -> 4096, 168 us instead of 138: the copy engine's work goes
-// by the box).
+// (four of 32 made the gate/up kernel above 30 us longer: the copy engine's work goes by the box).
 #pragma once
 
 #include "gemm_tc.cuh"
@@ -562,7 +569,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 }
 
 // Codes and scales of the rows that the groups hold (h between the two products); rows outside every group are not
-// read.  A row per TPR threads, the filled rows dealt over a fixed grid.
+// read.  A row per TPR threads, the filled rows dealt over a fixed grid.  Bound by HBM: 16384 rows of 4096 in 31 to 38
+// us (201 MB).
 template <int TPR, int NV>
 __global__ void __launch_bounds__(256) k_quant_groups(const __nv_bfloat16* __restrict__ x, const I8Params p,
                                                       int8_t* __restrict__ q, float* __restrict__ scale) {

@@ -132,6 +132,8 @@ __global__ void __launch_bounds__(256, KMAX <= 4 ? 5 : KMAX <= 8 ? 3 : 2) k_comb
 
 // dx_t = sum over the kept slots of dx_perm rows (slot order, fp32), plus add_t when given; one thread per eight
 // columns of a token, its k row loads issued together.  `add` may be dx itself: the thread reads its slice first.
+// Bound by HBM: 32768 tokens of width 768, top-4, bf16 in 40.5 us (6.2 TB/s); 1500 of width 7168, top-8, fp32 with an
+// addend in 66 us (6.5 TB/s).
 template <int KMAX, typename TIn, typename TOut>
 __global__ void __launch_bounds__(256) k_permute_bwd(const TIn* __restrict__ dx_perm,
                                                      const int32_t* __restrict__ slot_pos, const TOut* add, TOut* dx,
