@@ -16,6 +16,7 @@ Nothing is kept from the forward but its inputs: the backward recomputes the rou
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (MoeShape, moe_backward, moe_combine, moe_combine_backward, moe_forward, moe_permute,
                moe_permute_backward)
@@ -68,6 +69,7 @@ class DispatchFunction(torch.autograd.Function):
         return p["x_perm"], p["slot_pos"], p["kept"], p["offsets"]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dx_perm, _dslot, _dkept, _doffsets):
         slot_pos, = ctx.saved_tensors
         return None, moe_permute_backward(ctx.shape, dx_perm.contiguous(), slot_pos, dtype=torch.bfloat16), None
@@ -90,6 +92,7 @@ class CombineFunction(torch.autograd.Function):
         return moe_combine(shape, y_perm, slot_pos, topk_w, y_shared)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         y_perm, slot_pos, topk_w, kept = ctx.saved_tensors
         dout = dout.contiguous()

@@ -93,7 +93,8 @@ def test_leading_dimensions_and_given_outputs(lib):
                                               # either side of the one-launch form's 4096 pairs, its three widths
                                               (4096, 512, 1, 64, 0, 0.5), (4097, 512, 1, 64, 0, 0.5),
                                               (256, 20, 16, 528, 60, 0.6), (257, 20, 16, 528, 60, 0.6),
-                                              (100, 7, 5, 1056, 0, 0.0), (256, 384, 8, 256, 2, 1.0)])
+                                              (100, 7, 5, 1056, 0, 0.0), (256, 384, 8, 256, 2, 1.0),
+                                              (600, 16, 8, 1056, 250, 0.5)])
 def test_permute_int8_matches_the_oracle(lib, T, E, k, d, cap, skew):
     moe = lib
     s = moe.MoeShape(T=T, d=d, E=E, k=k, H=16, capacity=cap, wfmt=moe.WFMT_INT8)
@@ -203,6 +204,41 @@ def test_pair_and_single_tiles_give_the_same_bits(lib):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("rows", [100, 200])
+@pytest.mark.parametrize("act", [0, 1])
+def test_fused_and_separate_kernels_give_the_same_bits(lib, rows, act):
+    """One expert of 768 x 256 alone is run by separate kernels, 60 copies of it with the same rows by the fused one, on
+    single CTAs (100 rows a group) and on pairs (200)."""
+    moe = lib
+    d, H, n = 768, 256, 60
+    w = _experts(1, d, H, 7)
+    x = torch.randn(rows, d, generator=torch.Generator().manual_seed(rows)).bfloat16().to(DEV)
+    xq, xs = moe.moe_quantize_int8(x)
+    s = moe.MoeShape(T=n * rows, d=d, E=n, k=1, H=H, act=act, wfmt=moe.WFMT_INT8)
+    one = {k_: v.to(DEV) for k_, v in w.items()}
+    many = {k_: v.to(DEV).repeat(n, *[1] * (v.dim() - 1)).contiguous() for k_, v in w.items()}
+    st = (torch.arange(n, dtype=torch.int32) * rows).to(DEV)
+    ro = torch.full((n,), rows, dtype=torch.int32, device=DEV)
+    before = moe.moe_launch_count()
+    a = moe.moe_expert_ffn_int8(s, xq, xs, **one)
+    mid = moe.moe_launch_count()
+    b = moe.moe_expert_ffn_int8(s, xq.repeat(n, 1), xs.repeat(n), **many, group_start=st, group_rows=ro)
+    assert (mid - before, moe.moe_launch_count() - mid) == (3, 1)
+    assert torch.equal(b.view(n, rows, d), a.expand(n, rows, d))
+
+
+@pytest.mark.parametrize("R,d,H,act", [(3000, 192, 512, 0), (129, 1040, 320, 1), (1, 4096, 1024, 0)])
+def test_one_dense_group_without_a_table(lib, R, d, H, act):
+    moe = lib
+    w = _experts(1, d, H, 3)
+    x = torch.randn(R, d, generator=torch.Generator().manual_seed(R)).bfloat16()
+    s = moe.MoeShape(T=R, d=d, E=1, k=1, H=H, act=act, wfmt=moe.WFMT_INT8)
+    dv = {k_: v.to(DEV) for k_, v in w.items()}
+    got = moe.moe_expert_ffn(s, x.to(DEV), dv["w13"], dv["w2"], s13=dv["s13"], s2=dv["s2"])[1]
+    q, sc = O.quantize_rows_int8(np64(x))
+    _check_rows(np64(got), q, sc, w, 0, act, "dense")
+
+
 def test_slabs_overlong_groups_and_untouched_rows(lib):
     moe = lib
     # capacity slabs with rows behind the filled ones; groups out of order; the last one runs past the buffer
@@ -306,7 +342,8 @@ def _forward(moe, s, dv, **kw):
 
 @pytest.mark.parametrize("T,d,E,k,H,H_s,cap,act", [(256, 64, 8, 2, 128, 64, 0, 0), (1, 512, 16, 4, 256, 0, 0, 0),
                                                    (500, 192, 24, 3, 80, 48, 70, 1), (700, 128, 4, 2, 256, 128, 0, 0),
-                                                   (64, 1024, 48, 8, 512, 256, 0, 1)])
+                                                   (64, 1024, 48, 8, 512, 256, 0, 1),
+                                                   (520, 1056, 16, 8, 64, 32, 300, 0)])
 def test_layer_matches_the_oracle_and_its_steps(lib, T, d, E, k, H, H_s, cap, act):
     moe = lib
     s, inp, w, sh, dv = _layer(moe, T, d, E, k, H, H_s, cap, act, seed=T)
@@ -352,6 +389,14 @@ def test_layer_in_a_graph_and_on_another_stream(lib):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+    # with the shared expert on a second stream, captured too
+    two, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(two):
+        out2 = _forward(moe, s, dv, ws=ws, side_stream=side)["out"]
+    ws.fill_(255)
+    two.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out2, want)
     # the steps on a stream of their own, scratch and outputs allocated for it
     idx = _forward(moe, s, dv, ws=ws)["topk_idx"]
     a = moe.moe_permute_int8(s, dv["x"], idx, full=True)

@@ -101,18 +101,20 @@ def test_int8_forward_needs_its_scales(L):
 def test_sorting_gradient_refusals(L):
     s, cap = _shape(wfmt=0), _shape(wfmt=0, capacity=16)
 
-    def cb(sh=s, dout=FAKE, y=FAKE, slot=FAKE, w=FAKE, kept=None, dy=FAKE, dw=FAKE):
+    def cb(sh=s, dout=P(8192), y=P(8192), slot=FAKE, w=FAKE, kept=None, dy=FAKE, dw=FAKE):
         return L.moe_combine_backward(ctypes.byref(sh), dout, y, slot, w, kept, dy, dw, None)
     assert cb(dout=None) == 1 and cb(slot=None) == 1 and cb(w=None) == 1
     assert cb(y=None) == 1 and cb(dy=None, dw=None) == 1
     assert cb(kept=FAKE) == 1 and cb(sh=cap, kept=FAKE, dy=None) == 1
     assert cb(dout=P(4104)) == 1 and cb(y=P(4104)) == 1 and cb(dy=P(4104)) == 1
     assert cb(sh=_shape(d=72)) == 2
+    assert cb(dout=P(8192), y=FAKE, dy=FAKE) == 1 and cb(dout=FAKE, y=P(8192), dy=FAKE) == 1     # in place
 
-    def pb(g=FAKE, ti=0, slot=FAKE, add=None, dx=FAKE, to=0):
+    def pb(g=P(8192), ti=0, slot=FAKE, add=None, dx=FAKE, to=0):
         return L.moe_permute_backward(ctypes.byref(s), g, ti, slot, add, dx, to, None)
     assert pb(g=None) == 1 and pb(slot=None) == 1 and pb(dx=None) == 1
     assert pb(ti=2) == 1 and pb(to=-1) == 1
+    assert pb(g=FAKE, dx=FAKE) == 1                                                               # in place
     assert pb(g=P(4104)) == 1 and pb(add=P(4104)) == 1 and pb(dx=P(4104)) == 1
 
 
@@ -229,6 +231,9 @@ def test_gradients_through_dispatch_and_combine(monkeypatch, cap):
         return ag.combine(s, torch.tanh(xp), slot, w, ysh, kept=kept if cap else None)
     assert torch.autograd.gradcheck(run, (x, w, ysh))
     assert (calls["kept"] is not None) == bool(cap) and calls["want_dw"] and calls["dtype"] == torch.bfloat16
+    with pytest.raises(RuntimeError):           # no second derivatives
+        g1, = torch.autograd.grad(run(x, w, ysh).sum(), x, create_graph=True)
+        g1.sum().backward()
     xp, slot, kept, offs = ag.dispatch(s, x, idx)
     assert xp.requires_grad and not slot.requires_grad and not kept.requires_grad and not offs.requires_grad
     ag.combine(s, torch.tanh(xp), slot, w.detach(), None, kept=kept if cap else None).sum().backward()
