@@ -176,8 +176,10 @@ __device__ __forceinline__ float2 i8_scaled(uint32_t v0, uint32_t v1, float row,
 }
 
 // act(g) u of two columns, in packed fp32 pairs.  SiLU: g / (1 + exp(-g)).  GELU: g Phi(g) = max(g, 0) - |g| Q(|g|)
-// with the normal tail Q(a) = erfc(a / sqrt 2) / 2 by Abramowitz & Stegun 7.1.26 (the factor 1/2 and the sqrt 2
-// folded into its coefficients); the tail form does not cancel for negative g.
+// with the normal tail Q; that form does not cancel for negative g.  Q(a) = exp(-a^2 / 2) t P(t), t = 1 / (1 + c a): P
+// has degree 6 and c = 0.26374, fitted so that the largest relative error over 0 <= a <= 13.3 is least (5.2e-7 before,
+// 1e-6 after the fp32 arithmetic; beyond, exp underflows).  The error is relative because a row whose gates all lie in
+// the tail is lifted back to full size by its scale.  (Two terms fewer leave 2.7e-5.)
 template <int MODE>
 __device__ __forceinline__ float2 i8_glu2(float2 g, float2 u) {
   auto both = [](float c) { return make_float2(c, c); };
@@ -187,12 +189,14 @@ __device__ __forceinline__ float2 i8_glu2(float2 g, float2 u) {
     return __fmul2_rn(__fmul2_rn(g, make_float2(rcp_approx(d.x), rcp_approx(d.y))), u);
   }
   const float2 a = make_float2(fabsf(g.x), fabsf(g.y));
-  const float2 d = __ffma2_rn(both(0.3275911f * 0.7071067811865476f), a, both(1.0f));
+  const float2 d = __ffma2_rn(both(0.26374f), a, both(1.0f));
   const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
-  float2 poly = __ffma2_rn(t, both(0.5f * 1.061405429f), both(-0.5f * 1.453152027f));
-  poly = __ffma2_rn(t, poly, both(0.5f * 1.421413741f));
-  poly = __ffma2_rn(t, poly, both(-0.5f * 0.284496736f));
-  poly = __ffma2_rn(t, poly, both(0.5f * 0.254829592f));
+  float2 poly = __ffma2_rn(t, both(-0.0696539249f), both(0.205525397f));
+  poly = __ffma2_rn(t, poly, both(-0.078861467f));
+  poly = __ffma2_rn(t, poly, both(0.150310451f));
+  poly = __ffma2_rn(t, poly, both(0.0797937966f));
+  poly = __ffma2_rn(t, poly, both(0.107823258f));
+  poly = __ffma2_rn(t, poly, both(0.105062232f));
   const float2 x = __fmul2_rn(__fmul2_rn(g, g), both(-0.7213475204444817f));
   const float2 q = __fmul2_rn(__fmul2_rn(t, poly), make_float2(ex2_approx(x.x), ex2_approx(x.y)));
   return __fmul2_rn(__ffma2_rn(make_float2(-a.x, -a.y), q, make_float2(fmaxf(g.x, 0.f), fmaxf(g.y, 0.f))), u);
