@@ -1595,6 +1595,11 @@ int moe_forward(const moe_shape* s, const void* x, const float* w_router, const 
   if (s->wfmt != MOE_WFMT_BF16 &&
       (!s13 || !s2 || !aligned16(s13) || !aligned16(s2) || (s->H_s > 0 && (!s13_sh || !s2_sh))))
     return MOE_INVALID_ARGUMENT;
+  if (s->H_s > 0) {
+    if (!aligned16(w13_sh) || !aligned16(w2_sh)) return MOE_INVALID_ARGUMENT;
+    // INT8 scales come by bulk copies; INT4 ones one at a time
+    if (s->wfmt == MOE_WFMT_INT8 && (!aligned16(s13_sh) || !aligned16(s2_sh))) return MOE_INVALID_ARGUMENT;
+  }
   const Workspace L = ws_layout(s);
   if (ws_bytes < L.total) return MOE_WORKSPACE_TOO_SMALL;
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
