@@ -18,6 +18,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -180,7 +181,14 @@ def _on(stream, *tensors):
     return ctx
 
 
-_ws_cache: dict = {}
+class _Held(threading.local):
+    """The scratch that workspace() keeps: device index -> (stream handle, buffer), one of each host thread."""
+
+    def __init__(self):
+        self.of = {}
+
+
+_held = _Held()
 
 
 def moe_workspace_size(shape: MoeShape) -> int:
@@ -190,14 +198,30 @@ def moe_workspace_size(shape: MoeShape) -> int:
 
 
 def workspace(shape: MoeShape, device=None) -> torch.Tensor:
-    """A cached device buffer of moe_workspace_size(shape) bytes (grown on demand, per device)."""
+    """A device buffer of moe_workspace_size(shape) bytes, for calls on the device's current stream.  Between calls of one
+    host thread on one stream it is kept and grown on demand.  A call on another stream, from another thread or under
+    graph capture gets a buffer of its own, allocated for that stream (or by the graph): scratch is never shared by
+    calls that may overlap."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    need = moe_workspace_size(shape)
-    buf = _ws_cache.get(dev)
-    if buf is None or buf.numel() < need:
-        buf = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        _ws_cache[dev] = buf
-    return buf
+    index = dev.index if dev.index is not None else torch.cuda.current_device()
+    need = max(moe_workspace_size(shape), 256)
+    with _HERE_CTX if index == torch.cuda.current_device() else torch.cuda.device(index):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=dev)
+        handle = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+        held = _held.of.get(index)
+        if held is None or held[0] != handle or held[1].numel() < need:
+            held = (handle, torch.empty(need, dtype=torch.uint8, device=dev))
+            _held.of[index] = held
+    return held[1]
+
+
+def _scratch(shape: MoeShape, dev, stream) -> torch.Tensor:
+    """workspace() for a call on `stream` (None: the current one)."""
+    if stream is None:
+        return workspace(shape, dev)
+    with torch.cuda.stream(stream):
+        return workspace(shape, dev)
 
 
 def moe_capacity(T: int, k: int, E: int, factor: float) -> int:
@@ -220,7 +244,7 @@ def moe_route(shape: MoeShape, x, w_router, bias=None, *, logits=False, aux=Fals
         out["aux_f"] = torch.empty(E, dtype=torch.float32, device=dev)
         out["aux_p"] = torch.empty(E, dtype=torch.float32, device=dev)
         out["aux"] = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = ws if ws is not None else workspace(shape, dev)
+    ws = ws if ws is not None else _scratch(shape, dev, stream)
     rc = _L().moe_route(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(out.get("logits")),
                         _ptr(out["topk_idx"]), _ptr(out["topk_w"]), _ptr(out["counts"]), _ptr(out.get("aux_f")),
                         _ptr(out.get("aux_p")), _ptr(out.get("aux")), _ptr(ws), ws.numel(), _stream(stream))
@@ -239,7 +263,7 @@ def moe_route_from_logits(shape: MoeShape, logits, *, aux=False, ws=None, stream
         out["aux_f"] = torch.empty(E, dtype=torch.float32, device=dev)
         out["aux_p"] = torch.empty(E, dtype=torch.float32, device=dev)
         out["aux"] = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = ws if ws is not None else workspace(shape, dev)
+    ws = ws if ws is not None else _scratch(shape, dev, stream)
     rc = _L().moe_route_from_logits(ctypes.byref(shape), _ptr(logits), _ptr(out["topk_idx"]), _ptr(out["topk_w"]),
                                     _ptr(out["counts"]), _ptr(out.get("aux_f")), _ptr(out.get("aux_p")),
                                     _ptr(out.get("aux")), _ptr(ws), ws.numel(), _stream(stream))
@@ -272,7 +296,7 @@ def moe_permute(shape: MoeShape, x, topk_idx, *, ws=None, stream=None, out=None)
         _want(out["x_perm"], torch.bfloat16, (shape.R, d), "out['x_perm']")
         _want(out["row_src"], torch.int32, (shape.R,), "out['row_src']")
         _want(out["slot_pos"], torch.int32, (T, k), "out['slot_pos']")
-    ws = ws if ws is not None else workspace(shape, dev)
+    ws = ws if ws is not None else _scratch(shape, dev, stream)
     rc = _L().moe_permute(ctypes.byref(shape), _ptr(x), _ptr(topk_idx), _ptr(out["slot_pos"]),
                           _ptr(out["drop_mask"]), _ptr(out["counts"]), _ptr(out["kept"]), _ptr(out["offsets"]),
                           _ptr(out["row_src"]), _ptr(out["x_perm"]), _ptr(ws), ws.numel(), _stream(stream))
@@ -376,7 +400,7 @@ def moe_forward(shape: MoeShape, x, w_router, w13, w2, *, bias=None, s13=None, s
         r.update(aux_f=torch.empty(E, dtype=torch.float32, device=dev),
                  aux_p=torch.empty(E, dtype=torch.float32, device=dev),
                  aux=torch.empty(1, dtype=torch.float32, device=dev))
-    ws = ws if ws is not None else workspace(shape, dev)
+    ws = ws if ws is not None else _scratch(shape, dev, stream)
     rc = _L().moe_forward(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w13), _ptr(s13), _ptr(w2),
                           _ptr(s2), _ptr(w13_sh), _ptr(s13_sh), _ptr(w2_sh), _ptr(s2_sh), _ptr(out),
                           _ptr(r.get("topk_idx")), _ptr(r.get("topk_w")), _ptr(r.get("counts")),
