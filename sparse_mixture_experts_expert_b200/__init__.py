@@ -289,17 +289,17 @@ def moe_permute(shape: MoeShape, x, topk_idx, *, ws=None, stream=None, out=None)
     T, d, E, k = shape.T, shape.d, shape.E, shape.k
     _want(x, torch.bfloat16, (T, d), "x")
     _want(topk_idx, torch.int32, (T, k), "topk_idx")
-    dev = x.device
-    if out is None:
-        out = permute_outputs(shape, dev)
-    else:
-        _want(out["x_perm"], torch.bfloat16, (shape.R, d), "out['x_perm']")
-        _want(out["row_src"], torch.int32, (shape.R,), "out['row_src']")
-        _want(out["slot_pos"], torch.int32, (T, k), "out['slot_pos']")
-    ws = ws if ws is not None else _scratch(shape, dev, stream)
-    rc = _L().moe_permute(ctypes.byref(shape), _ptr(x), _ptr(topk_idx), _ptr(out["slot_pos"]),
-                          _ptr(out["drop_mask"]), _ptr(out["counts"]), _ptr(out["kept"]), _ptr(out["offsets"]),
-                          _ptr(out["row_src"]), _ptr(out["x_perm"]), _ptr(ws), ws.numel(), _stream(stream))
+    with _on(stream, x, topk_idx, ws, None if out is None else out["x_perm"]):
+        if out is None:
+            out = permute_outputs(shape, x.device)
+        else:
+            _want(out["x_perm"], torch.bfloat16, (shape.R, d), "out['x_perm']")
+            _want(out["row_src"], torch.int32, (shape.R,), "out['row_src']")
+            _want(out["slot_pos"], torch.int32, (T, k), "out['slot_pos']")
+        ws = ws if ws is not None else workspace(shape, x.device)
+        rc = _L().moe_permute(ctypes.byref(shape), _ptr(x), _ptr(topk_idx), _ptr(out["slot_pos"]),
+                              _ptr(out["drop_mask"]), _ptr(out["counts"]), _ptr(out["kept"]), _ptr(out["offsets"]),
+                              _ptr(out["row_src"]), _ptr(out["x_perm"]), _ptr(ws), ws.numel(), _stream())
     _check(rc, "moe_permute")
     return out
 
@@ -363,10 +363,11 @@ def moe_combine(shape: MoeShape, y_perm, slot_pos, topk_w, y_shared=None, *, out
     _want(topk_w, torch.float32, (T, k), "topk_w")
     if y_shared is not None:
         _want(y_shared, torch.bfloat16, (T, d), "y_shared")
-    if out is None:
-        out = torch.empty(shape.T, shape.d, dtype=torch.bfloat16, device=y_perm.device)
-    rc = _L().moe_combine(ctypes.byref(shape), _ptr(y_perm), _ptr(slot_pos), _ptr(topk_w), _ptr(y_shared),
-                          _ptr(out), _stream(stream))
+    with _on(stream, y_perm, slot_pos, topk_w, y_shared, out):
+        if out is None:
+            out = torch.empty(T, d, dtype=torch.bfloat16, device=y_perm.device)
+        rc = _L().moe_combine(ctypes.byref(shape), _ptr(y_perm), _ptr(slot_pos), _ptr(topk_w), _ptr(y_shared),
+                              _ptr(out), _stream())
     _check(rc, "moe_combine")
     return out
 

@@ -1,0 +1,96 @@
+"""The grouping and the combine run on their tensors' device and, where one is given, on their stream (no GPU: tensors
+and devices are stand-ins)."""
+
+import contextlib
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import sparse_mixture_experts_expert_b200 as moe
+
+
+class Fake:
+    """A tensor of a device that is not there."""
+
+    def __init__(self, dev, shape, dtype):
+        self.device, self.shape, self.dtype, self.is_cuda = torch.device(dev), torch.Size(shape), dtype, True
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    now = SimpleNamespace(dev=0, stream=None, log=[])
+
+    @contextlib.contextmanager
+    def device(d):
+        old, now.dev = now.dev, torch.device(d).index
+        yield
+        now.dev = old
+
+    @contextlib.contextmanager
+    def on_stream(st):
+        old, now.stream = now.stream, st
+        yield
+        now.stream = old
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now.dev)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "stream", on_stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(moe, "_raw_stream", lambda dev: 100 + dev if now.stream is None else now.stream.cuda_stream)
+    made = lambda *sh, dtype=None, device=None: (now.log.append(("made", now.dev, now.stream)),     # noqa: E731
+                                                 Fake(device, sh, dtype))[1]
+    for name in ("empty", "zeros"):
+        monkeypatch.setattr(torch, name, made)
+    monkeypatch.setattr(torch, "full", lambda sh, v, dtype=None, device=None: made(*sh, dtype=dtype, device=device))
+    monkeypatch.setattr(moe, "moe_workspace_size", lambda shape: 512)
+    monkeypatch.setattr(moe, "_held", type(moe._held)())
+    run = lambda *a: (now.log.append(("ran", now.dev, a[-1])), 0)[1]                                 # noqa: E731
+    monkeypatch.setattr(moe, "_L", lambda: SimpleNamespace(moe_permute=run, moe_combine=run))
+    return now
+
+
+def _args(dev, T=4, k=2, d=64):
+    f = lambda sh, dt: Fake(dev, sh, dt)  # noqa: E731
+    return (moe.MoeShape(T=T, d=d, E=8, k=k, H=16), f((T, d), torch.bfloat16), f((T, k), torch.int32),
+            f((T * k, d), torch.bfloat16), f((T, k), torch.float32))
+
+
+def test_tensors_of_another_device_run_there(calls):
+    s, x, idx, y, w = _args("cuda:1")
+    moe.moe_permute(s, x, idx)
+    moe.moe_combine(s, y, idx, w)
+    assert [e for e in calls.log if e[0] == "ran"] == [("ran", 1, 101)] * 2
+    assert all(e[1] == 1 for e in calls.log) and calls.dev == 0
+
+
+def test_tensors_of_two_devices_are_refused(calls):
+    s, x, idx, y, w = _args("cuda:1")
+    other = Fake("cuda:0", idx.shape, idx.dtype)
+    with pytest.raises(ValueError, match="cuda:0"):
+        moe.moe_permute(s, x, other)
+    with pytest.raises(ValueError, match="cuda:0"):
+        moe.moe_combine(s, y, other, w)
+    with pytest.raises(ValueError, match="cuda:0"):
+        moe.moe_combine(s, y, idx, w, out=Fake("cuda:0", (4, 64), torch.bfloat16))
+    assert not [e for e in calls.log if e[0] == "ran"]
+
+
+def test_outputs_are_prepared_on_the_given_stream(calls):
+    # row_src and x_perm are filled before the rows are moved: on the same stream, or the fill may come after
+    s, x, idx, y, w = _args("cuda:0")
+    st = SimpleNamespace(device=torch.device("cuda:0"), cuda_stream=55)
+    moe.moe_permute(s, x, idx, stream=st)
+    made = [e for e in calls.log if e[0] == "made"]
+    assert len(made) == 8 and all(e[2] is st for e in made) and ("ran", 0, 55) in calls.log
