@@ -154,6 +154,14 @@ def _want(t, dtype, shape, name):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _holds(t, dtype, n, name, more=True):
+    """t holds the n values that are read or written from its first on (more: it may hold others behind them)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() < n or (t.numel() > n and not more):
+        raise ValueError(f"{name}: expected {'at least ' if more else ''}{n} values, got shape {tuple(t.shape)}")
+
+
 _HERE_CTX = contextlib.nullcontext()
 
 
@@ -357,12 +365,16 @@ def moe_expert_ffn(shape: MoeShape, x_grouped, w13, w2, *, hidden=None, group_st
 
 
 def moe_combine(shape: MoeShape, y_perm, slot_pos, topk_w, y_shared=None, *, out=None, stream=None):
+    """Weighted top-k reduction back to token order: out [T, d] bf16.  y_perm, slot_pos, topk_w and ``out`` may be larger
+    buffers or have other leading dimensions ([E, capacity, d], flat): their first R d, T k, T k and T d values count."""
     T, d, k = shape.T, shape.d, shape.k
-    _want(y_perm, torch.bfloat16, (shape.R, d), "y_perm")
-    _want(slot_pos, torch.int32, (T, k), "slot_pos")
-    _want(topk_w, torch.float32, (T, k), "topk_w")
+    _holds(y_perm, torch.bfloat16, shape.R * d, "y_perm")
+    _holds(slot_pos, torch.int32, T * k, "slot_pos")
+    _holds(topk_w, torch.float32, T * k, "topk_w")
     if y_shared is not None:
-        _want(y_shared, torch.bfloat16, (T, d), "y_shared")
+        _holds(y_shared, torch.bfloat16, T * d, "y_shared", more=False)
+    if out is not None:
+        _holds(out, torch.bfloat16, T * d, "out")
     with _on(stream, y_perm, slot_pos, topk_w, y_shared, out):
         if out is None:
             out = torch.empty(T, d, dtype=torch.bfloat16, device=y_perm.device)

@@ -109,4 +109,9 @@ def combine(shape: MoeShape, y_perm, slot_pos, topk_w, y_shared=None, kept=None)
     dispatch), so that the gradient of rows that no token fills is zero."""
     if shape.capacity > 0 and kept is None and y_perm.requires_grad:
         raise ValueError("combine: with a capacity, the gradient of y_perm needs kept")
+    dims = dict(y_perm=(shape.R, shape.d), slot_pos=(shape.T, shape.k), topk_w=(shape.T, shape.k),
+                y_shared=(shape.T, shape.d))
+    for (name, want), t in zip(dims.items(), (y_perm, slot_pos, topk_w, y_shared)):
+        if t is not None and tuple(t.shape) != want:   # the gradients' shapes
+            raise ValueError(f"combine: {name}: expected shape {want}, got {tuple(t.shape)}")
     return CombineFunction.apply(shape, y_perm, slot_pos, topk_w, y_shared, kept)
