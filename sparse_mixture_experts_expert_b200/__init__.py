@@ -604,10 +604,13 @@ def moe_expert_ffn_int8(shape: MoeShape, xq, xs, w13, s13, w2, s2, *, hidden=Non
     return y
 
 
-def moe_combine_backward(shape: MoeShape, dout, y_perm, slot_pos, topk_w, *, kept=None, want_dw=True, stream=None):
-    """Gradient of moe_combine: dict(dy_perm [R, d] bf16, dtopk_w [T, k] fp32 or None); that of y_shared is dout.
-    With a capacity and ``kept`` (of moe_permute), rows that no token fills come back zero; without ``kept`` they
-    hold nothing in particular."""
+def moe_combine_backward(shape: MoeShape, dout, y_perm, slot_pos, topk_w, *, kept=None, want_dw=True, want_dy=True,
+                         stream=None):
+    """Gradient of moe_combine: dict(dy_perm [R, d] bf16, dtopk_w [T, k] fp32), None for one that is not wanted; that
+    of y_shared is dout.  With a capacity and ``kept`` (of moe_permute), rows that no token fills come back zero;
+    without ``kept`` they hold nothing in particular."""
+    if not (want_dw or want_dy):
+        raise ValueError("moe_combine_backward: neither want_dw nor want_dy")
     T, d, k, R = shape.T, shape.d, shape.k, shape.R
     _want(dout, torch.bfloat16, (T, d), "dout")
     _want(y_perm, torch.bfloat16, (R, d), "y_perm")
@@ -616,10 +619,11 @@ def moe_combine_backward(shape: MoeShape, dout, y_perm, slot_pos, topk_w, *, kep
     if kept is not None:
         _want(kept, torch.int32, (shape.E,), "kept")
     with _on(stream, dout, y_perm, slot_pos, topk_w, kept):
-        dy = torch.empty_like(y_perm)
+        dy = torch.empty_like(y_perm) if want_dy else None
         dw = torch.empty_like(topk_w) if want_dw else None
         rc = _L().moe_combine_backward(ctypes.byref(shape), _ptr(dout), _ptr(y_perm), _ptr(slot_pos), _ptr(topk_w),
-                                       _ptr(kept) if shape.capacity > 0 else None, _ptr(dy), _ptr(dw), _stream())
+                                       _ptr(kept) if want_dy and shape.capacity > 0 else None, _ptr(dy), _ptr(dw),
+                                       _stream())
         _check(rc, "moe_combine_backward")
     return dict(dy_perm=dy, dtopk_w=dw)
 

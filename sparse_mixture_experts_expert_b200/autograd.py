@@ -98,9 +98,11 @@ class CombineFunction(torch.autograd.Function):
         dout = dout.contiguous()
         need_y, need_w, need_sh = ctx.needs_input_grad[1], ctx.needs_input_grad[3], ctx.needs_input_grad[4]
         g = dict(dy_perm=None, dtopk_w=None)
-        if need_y or need_w:
+        if need_y:
             g = moe_combine_backward(ctx.shape, dout, y_perm, slot_pos, topk_w, kept=kept if ctx.has_kept else None,
                                      want_dw=need_w)
+        elif need_w:   # frozen rows: no buffer of their size
+            g = moe_combine_backward(ctx.shape, dout, y_perm, slot_pos, topk_w, want_dy=False)
         return None, g["dy_perm"], None, g["dtopk_w"], dout if need_sh else None, None
 
 
