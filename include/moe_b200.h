@@ -232,7 +232,7 @@ int moe_quantize_int8(const void* x, int32_t dtype, int64_t rows, int32_t K, int
  * moe_permute with the rows quantised on the way (moe_quantize_int8 of x[t]): each token is read and quantised once,
  * and its codes and scale written to the row of each kept slot.
  *   xq_perm [R, d] int8   out,  xs_perm [R] fp32   out   unfilled rows untouched
- * Other arguments, rules and errors as moe_permute (any wfmt).
+ * Other arguments, rules and errors as moe_permute (any wfmt); slot_pos over topk_idx gives MOE_INVALID_ARGUMENT.
  */
 int moe_permute_int8(const moe_shape* s, const void* x, const int32_t* topk_idx, int32_t* slot_pos,
                      uint8_t* drop_mask, int32_t* counts, int32_t* kept, int32_t* offsets, int32_t* row_src,

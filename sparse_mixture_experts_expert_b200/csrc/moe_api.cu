@@ -80,6 +80,11 @@ static cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
   } while (0)
 
 static inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// na bytes at a and nb bytes at b have a byte in common (a NULL has none)
+static inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+}
 static inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 static inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
@@ -1967,6 +1972,8 @@ int moe_permute_int8(const moe_shape* s, const void* x, const int32_t* topk_idx,
     return MOE_INVALID_ARGUMENT;
   const Workspace L = ws_layout(s);
   if (ws_bytes < L.total) return MOE_WORKSPACE_TOO_SMALL;
+  const size_t pairs = (size_t)s->T * s->k * 4;   // read by every CTA of the one-launch form while others write
+  if (overlap(topk_idx, pairs, slot_pos, pairs)) return MOE_INVALID_ARGUMENT;
   if (s->T * s->k <= kSmallPairs)
     return launch_permute_quant_small(s, x, topk_idx, slot_pos, drop_mask, counts, kept, offsets, row_src, xq_perm,
                                       xs_perm, stream);
