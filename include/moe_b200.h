@@ -270,7 +270,7 @@ int moe_expert_ffn_int8(const moe_shape* s, int32_t n_groups, int32_t hidden, in
  *   dy_perm  [R, d] bf16 / NULL out  dy_perm[slot_pos[t,j]] = topk_w[t,j] dout_t, one rounding
  *   dtopk_w  [T, k] fp32 / NULL out  <dout_t, y_perm[slot_pos[t,j]]> in fp32, 0 where dropped
  * dy_perm may overlap neither y_perm nor dout.  Deterministic.  Errors: MOE_INVALID_ARGUMENT when both outputs are
- * NULL, for kept without a capacity or dy_perm, and for dy_perm equal to an input.
+ * NULL, for kept without a capacity or dy_perm, and for dy_perm over an input.
  */
 int moe_combine_backward(const moe_shape* s, const void* dout, const void* y_perm, const int32_t* slot_pos,
                          const float* topk_w, const int32_t* kept, void* dy_perm, float* dtopk_w,
@@ -282,7 +282,8 @@ int moe_combine_backward(const moe_shape* s, const void* dout, const void* y_per
  *   dx_perm  [R, d] bf16 or fp32 (in_dtype, enum moe_dtype)    in
  *   slot_pos [T, k] int32                                      in   outside [0, R): dropped, contributes nothing
  *   add      [T, d] out_dtype, or NULL                         in   may be dx itself (accumulation)
- *   dx       [T, d] bf16 or fp32 (out_dtype)                   out  may not overlap dx_perm
+ *   dx       [T, d] bf16 or fp32 (out_dtype)                   out
+ * Errors: MOE_INVALID_ARGUMENT for dx over dx_perm, or over add without being it.
  */
 int moe_permute_backward(const moe_shape* s, const void* dx_perm, int32_t in_dtype, const int32_t* slot_pos,
                          const void* add, void* dx, int32_t out_dtype, moe_stream_t stream);

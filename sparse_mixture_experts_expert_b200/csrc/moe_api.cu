@@ -2035,7 +2035,9 @@ int moe_combine_backward(const moe_shape* s, const void* dout, const void* y_per
   if (rc) return rc;
   if (!dout || !slot_pos || !topk_w || (!dy_perm && !dtopk_w) || (dtopk_w && !y_perm)) return MOE_INVALID_ARGUMENT;
   if (kept && (!dy_perm || s->capacity == 0)) return MOE_INVALID_ARGUMENT;
-  if (dy_perm && (dy_perm == y_perm || dy_perm == dout)) return MOE_INVALID_ARGUMENT;
+  const size_t rows = (size_t)grouped_rows(s) * s->d * 2;
+  if (overlap(dy_perm, rows, y_perm, rows) || overlap(dy_perm, rows, dout, (size_t)s->T * s->d * 2))
+    return MOE_INVALID_ARGUMENT;
   if (!aligned16(dout) || !aligned16(y_perm) || !aligned16(dy_perm)) return MOE_INVALID_ARGUMENT;
   const __nv_bfloat16* g = reinterpret_cast<const __nv_bfloat16*>(dout);
   const __nv_bfloat16* y = reinterpret_cast<const __nv_bfloat16*>(y_perm);
@@ -2068,7 +2070,12 @@ int moe_permute_backward(const moe_shape* s, const void* dx_perm, int32_t in_dty
   if (rc) return rc;
   auto known = [](int32_t t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; };
   if (!known(in_dtype) || !known(out_dtype)) return MOE_INVALID_ARGUMENT;
-  if (!dx_perm || !slot_pos || !dx || dx == dx_perm) return MOE_INVALID_ARGUMENT;
+  if (!dx_perm || !slot_pos || !dx) return MOE_INVALID_ARGUMENT;
+  auto bytes = [&](long long n, int32_t t) { return (size_t)n * s->d * (t == MOE_DTYPE_F32 ? 4 : 2); };
+  const size_t out_bytes = bytes(s->T, out_dtype);
+  if (overlap(dx, out_bytes, dx_perm, bytes(grouped_rows(s), in_dtype)) ||
+      (add != dx && overlap(dx, out_bytes, add, out_bytes)))
+    return MOE_INVALID_ARGUMENT;
   if (!aligned16(dx_perm) || !aligned16(add) || !aligned16(dx)) return MOE_INVALID_ARGUMENT;
   const int R = (int)grouped_rows(s);
   const unsigned blocks = (unsigned)cdiv(s->T * (long long)(s->d / 8), 256);
