@@ -148,6 +148,8 @@ def _stream(stream=None):
 
 
 def _want(t, dtype, shape, name):
+    if t is None:
+        raise ValueError(f"{name}: missing")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != tuple(shape):
@@ -347,6 +349,7 @@ def moe_expert_ffn(shape: MoeShape, x_grouped, w13, w2, *, hidden=None, group_st
         if h is not None:
             raise ValueError("moe_expert_ffn: INT8 experts return no h")
         _want(x_grouped, torch.bfloat16, (x_grouped.shape[0], shape.d), "x_grouped")
+        _want_experts(shape, hidden, w13, s13, w2, s2)
         xq, xs = moe_quantize_int8(x_grouped, stream=stream)
         return None, moe_expert_ffn_int8(shape, xq, xs, w13, s13, w2, s2, hidden=hidden, group_start=group_start,
                                          group_rows=group_rows, y=y, stream=stream)
@@ -391,15 +394,9 @@ def moe_forward(shape: MoeShape, x, w_router, w13, w2, *, bias=None, s13=None, s
     T, d, E, k = shape.T, shape.d, shape.E, shape.k
     _want(x, torch.bfloat16, (T, d), "x")
     if shape.wfmt == WFMT_INT8:
-        for n, H, sfx, ts in ((E, shape.H, "", (w13, s13, w2, s2)),
-                              (1, shape.H_s, "_sh", (w13_sh, s13_sh, w2_sh, s2_sh))):
-            if H == 0:
-                continue
-            for t, name, dtype, dims in zip(ts, ("w13", "s13", "w2", "s2"), (torch.int8, torch.float32) * 2,
-                                            ((n, 2 * H, d), (n, 2 * H), (n, d, H), (n, d))):
-                if t is None:
-                    raise ValueError(f"{name}{sfx}: missing")
-                _want(t, dtype, dims, name + sfx)
+        _want_experts(shape, shape.H, w13, s13, w2, s2, n=E)
+        if shape.H_s:
+            _want_experts(shape, shape.H_s, w13_sh, s13_sh, w2_sh, s2_sh, n=1, sfx="_sh")
     dev = x.device
     if out is None:
         out = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
@@ -572,19 +569,25 @@ def moe_permute_int8(shape: MoeShape, x, topk_idx, *, full=False, ws=None, strea
     return out
 
 
+def _want_experts(shape, hidden, w13, s13, w2, s2, n=None, sfx=""):
+    """INT8 weights and scales of n experts (None: as many as w13 holds) of this hidden width."""
+    if n is None and w13 is not None:
+        n = w13.shape[0]
+    for t, name, dtype, dims in ((w13, "w13", torch.int8, (n, 2 * hidden, shape.d)), (s13, "s13", torch.float32, (n, 2 * hidden)),
+                                 (w2, "w2", torch.int8, (n, shape.d, hidden)), (s2, "s2", torch.float32, (n, shape.d))):
+        _want(t, dtype, dims, name + sfx)
+
+
 def moe_expert_ffn_int8(shape: MoeShape, xq, xs, w13, s13, w2, s2, *, hidden=None, group_start=None,
                         group_rows=None, y=None, ws=None, stream=None):
     """Grouped gated expert FFN in 8-bit integers (shape.wfmt == WFMT_INT8): xq [R, d] int8 with one scale a row
     xs [R], w13 [n, 2 hidden, d] and w2 [n, d, hidden] int8 with one scale an output channel.  Returns y [R, d]
     bf16; rows outside every group are not written."""
     hidden = shape.H if hidden is None else hidden
-    n, R, d = w13.shape[0], xq.shape[0], shape.d
+    _want_experts(shape, hidden, w13, s13, w2, s2)
+    n, R, d = w13.shape[0], xq.shape[0] if xq is not None else 0, shape.d
     _want(xq, torch.int8, (R, d), "xq")
     _want(xs, torch.float32, (R,), "xs")
-    _want(w13, torch.int8, (n, 2 * hidden, d), "w13")
-    _want(w2, torch.int8, (n, d, hidden), "w2")
-    _want(s13, torch.float32, (n, 2 * hidden), "s13")
-    _want(s2, torch.float32, (n, d), "s2")
     for t, name in ((group_start, "group_start"), (group_rows, "group_rows")):
         if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < n):
             raise ValueError(f"{name}: expected at least {n} int32 values")
@@ -633,6 +636,8 @@ def moe_permute_backward(shape: MoeShape, dx_perm, slot_pos, *, add=None, dtype=
     """Gradient of moe_permute's row moves: dx [T, d] (dtype bf16 or fp32) = the sum of each token's kept rows of
     dx_perm [R, d] (bf16 or fp32), plus ``add`` [T, d] of that dtype when given.  ``out`` may be ``add``."""
     T, d, R = shape.T, shape.d, shape.R
+    if dx_perm is None:
+        raise ValueError("dx_perm: missing")
     if dx_perm.dtype not in DTYPE_CODE or dtype not in DTYPE_CODE:
         raise TypeError(f"dx_perm, dtype: expected torch.bfloat16 or torch.float32, got {dx_perm.dtype}, {dtype}")
     _want(dx_perm, dx_perm.dtype, (R, d), "dx_perm")
