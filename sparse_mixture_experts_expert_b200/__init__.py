@@ -244,20 +244,21 @@ def moe_route(shape: MoeShape, x, w_router, bias=None, *, logits=False, aux=Fals
     T, d, E, k = shape.T, shape.d, shape.E, shape.k
     _want(x, torch.bfloat16, (T, d), "x")
     _want(w_router, torch.float32, (E, d), "w_router")
-    dev = x.device
-    out = dict(topk_idx=torch.empty(T, k, dtype=torch.int32, device=dev),
-               topk_w=torch.empty(T, k, dtype=torch.float32, device=dev),
-               counts=torch.empty(E, dtype=torch.int32, device=dev))
-    if logits:
-        out["logits"] = torch.empty(T, E, dtype=torch.float32, device=dev)
-    if aux:
-        out["aux_f"] = torch.empty(E, dtype=torch.float32, device=dev)
-        out["aux_p"] = torch.empty(E, dtype=torch.float32, device=dev)
-        out["aux"] = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = ws if ws is not None else _scratch(shape, dev, stream)
-    rc = _L().moe_route(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(out.get("logits")),
-                        _ptr(out["topk_idx"]), _ptr(out["topk_w"]), _ptr(out["counts"]), _ptr(out.get("aux_f")),
-                        _ptr(out.get("aux_p")), _ptr(out.get("aux")), _ptr(ws), ws.numel(), _stream(stream))
+    with _on(None, x, w_router, bias, ws):
+        dev = x.device
+        out = dict(topk_idx=torch.empty(T, k, dtype=torch.int32, device=dev),
+                   topk_w=torch.empty(T, k, dtype=torch.float32, device=dev),
+                   counts=torch.empty(E, dtype=torch.int32, device=dev))
+        if logits:
+            out["logits"] = torch.empty(T, E, dtype=torch.float32, device=dev)
+        if aux:
+            out["aux_f"] = torch.empty(E, dtype=torch.float32, device=dev)
+            out["aux_p"] = torch.empty(E, dtype=torch.float32, device=dev)
+            out["aux"] = torch.empty(1, dtype=torch.float32, device=dev)
+        ws = ws if ws is not None else _scratch(shape, dev, stream)
+        rc = _L().moe_route(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(out.get("logits")),
+                            _ptr(out["topk_idx"]), _ptr(out["topk_w"]), _ptr(out["counts"]), _ptr(out.get("aux_f")),
+                            _ptr(out.get("aux_p")), _ptr(out.get("aux")), _ptr(ws), ws.numel(), _stream(stream))
     _check(rc, "moe_route")
     return out
 
@@ -265,18 +266,19 @@ def moe_route(shape: MoeShape, x, w_router, bias=None, *, logits=False, aux=Fals
 def moe_route_from_logits(shape: MoeShape, logits, *, aux=False, ws=None, stream=None):
     T, E, k = shape.T, shape.E, shape.k
     _want(logits, torch.float32, (T, E), "logits")
-    dev = logits.device
-    out = dict(topk_idx=torch.empty(T, k, dtype=torch.int32, device=dev),
-               topk_w=torch.empty(T, k, dtype=torch.float32, device=dev),
-               counts=torch.empty(E, dtype=torch.int32, device=dev))
-    if aux:
-        out["aux_f"] = torch.empty(E, dtype=torch.float32, device=dev)
-        out["aux_p"] = torch.empty(E, dtype=torch.float32, device=dev)
-        out["aux"] = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = ws if ws is not None else _scratch(shape, dev, stream)
-    rc = _L().moe_route_from_logits(ctypes.byref(shape), _ptr(logits), _ptr(out["topk_idx"]), _ptr(out["topk_w"]),
-                                    _ptr(out["counts"]), _ptr(out.get("aux_f")), _ptr(out.get("aux_p")),
-                                    _ptr(out.get("aux")), _ptr(ws), ws.numel(), _stream(stream))
+    with _on(None, logits, ws):
+        dev = logits.device
+        out = dict(topk_idx=torch.empty(T, k, dtype=torch.int32, device=dev),
+                   topk_w=torch.empty(T, k, dtype=torch.float32, device=dev),
+                   counts=torch.empty(E, dtype=torch.int32, device=dev))
+        if aux:
+            out["aux_f"] = torch.empty(E, dtype=torch.float32, device=dev)
+            out["aux_p"] = torch.empty(E, dtype=torch.float32, device=dev)
+            out["aux"] = torch.empty(1, dtype=torch.float32, device=dev)
+        ws = ws if ws is not None else _scratch(shape, dev, stream)
+        rc = _L().moe_route_from_logits(ctypes.byref(shape), _ptr(logits), _ptr(out["topk_idx"]), _ptr(out["topk_w"]),
+                                        _ptr(out["counts"]), _ptr(out.get("aux_f")), _ptr(out.get("aux_p")),
+                                        _ptr(out.get("aux")), _ptr(ws), ws.numel(), _stream(stream))
     _check(rc, "moe_route_from_logits")
     return out
 
@@ -390,33 +392,34 @@ def moe_combine(shape: MoeShape, y_perm, slot_pos, topk_w, y_shared=None, *, out
 def moe_forward(shape: MoeShape, x, w_router, w13, w2, *, bias=None, s13=None, s2=None, w13_sh=None, s13_sh=None,
                 w2_sh=None, s2_sh=None, out=None, routing=False, aux=False, ws=None, stream=None, side_stream=None):
     """The whole layer.  Returns ``out`` [T, d] bf16, or a dict with routing outputs when asked.
-    ``side_stream`` (a torch.cuda.Stream) lets a bf16 shared expert overlap the routing and routed experts."""
+    ``side_stream`` (a torch.cuda.Stream) lets a bf16 or INT8 shared expert overlap the routing and routed experts."""
     T, d, E, k = shape.T, shape.d, shape.E, shape.k
     _want(x, torch.bfloat16, (T, d), "x")
     if shape.wfmt == WFMT_INT8:
         _want_experts(shape, shape.H, w13, s13, w2, s2, n=E)
         if shape.H_s:
             _want_experts(shape, shape.H_s, w13_sh, s13_sh, w2_sh, s2_sh, n=1, sfx="_sh")
-    dev = x.device
-    if out is None:
-        out = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
-    r = {}
-    if routing:
-        r = dict(topk_idx=torch.empty(T, k, dtype=torch.int32, device=dev),
-                 topk_w=torch.empty(T, k, dtype=torch.float32, device=dev),
-                 counts=torch.empty(E, dtype=torch.int32, device=dev),
-                 drop_mask=torch.empty(T, k, dtype=torch.uint8, device=dev))
-    if aux:
-        r.update(aux_f=torch.empty(E, dtype=torch.float32, device=dev),
-                 aux_p=torch.empty(E, dtype=torch.float32, device=dev),
-                 aux=torch.empty(1, dtype=torch.float32, device=dev))
-    ws = ws if ws is not None else _scratch(shape, dev, stream)
-    rc = _L().moe_forward(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w13), _ptr(s13), _ptr(w2),
-                          _ptr(s2), _ptr(w13_sh), _ptr(s13_sh), _ptr(w2_sh), _ptr(s2_sh), _ptr(out),
-                          _ptr(r.get("topk_idx")), _ptr(r.get("topk_w")), _ptr(r.get("counts")),
-                          _ptr(r.get("drop_mask")), _ptr(r.get("aux_f")), _ptr(r.get("aux_p")), _ptr(r.get("aux")),
-                          _ptr(ws), ws.numel(), _stream(stream),
-                          ctypes.c_void_p(side_stream.cuda_stream) if side_stream is not None else None)
+    with _on(None, x, w_router, bias, w13, s13, w2, s2, w13_sh, s13_sh, w2_sh, s2_sh, out, ws):
+        dev = x.device
+        if out is None:
+            out = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
+        r = {}
+        if routing:
+            r = dict(topk_idx=torch.empty(T, k, dtype=torch.int32, device=dev),
+                     topk_w=torch.empty(T, k, dtype=torch.float32, device=dev),
+                     counts=torch.empty(E, dtype=torch.int32, device=dev),
+                     drop_mask=torch.empty(T, k, dtype=torch.uint8, device=dev))
+        if aux:
+            r.update(aux_f=torch.empty(E, dtype=torch.float32, device=dev),
+                     aux_p=torch.empty(E, dtype=torch.float32, device=dev),
+                     aux=torch.empty(1, dtype=torch.float32, device=dev))
+        ws = ws if ws is not None else _scratch(shape, dev, stream)
+        rc = _L().moe_forward(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w13), _ptr(s13), _ptr(w2),
+                              _ptr(s2), _ptr(w13_sh), _ptr(s13_sh), _ptr(w2_sh), _ptr(s2_sh), _ptr(out),
+                              _ptr(r.get("topk_idx")), _ptr(r.get("topk_w")), _ptr(r.get("counts")),
+                              _ptr(r.get("drop_mask")), _ptr(r.get("aux_f")), _ptr(r.get("aux_p")), _ptr(r.get("aux")),
+                              _ptr(ws), ws.numel(), _stream(stream),
+                              ctypes.c_void_p(side_stream.cuda_stream) if side_stream is not None else None)
     _check(rc, "moe_forward")
     if r:
         r["out"] = out

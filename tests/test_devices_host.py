@@ -57,7 +57,9 @@ def calls(monkeypatch):
     monkeypatch.setattr(moe, "moe_workspace_size", lambda shape: 512)
     monkeypatch.setattr(moe, "_held", type(moe._held)())
     run = lambda *a: (now.log.append(("ran", now.dev, a[-1])), 0)[1]                                 # noqa: E731
-    monkeypatch.setattr(moe, "_L", lambda: SimpleNamespace(moe_permute=run, moe_combine=run))
+    fwd = lambda *a: (now.log.append(("ran", now.dev, a[-2])), 0)[1]                                 # noqa: E731
+    monkeypatch.setattr(moe, "_L", lambda: SimpleNamespace(moe_permute=run, moe_combine=run, moe_route=run,
+                                                                 moe_route_from_logits=run, moe_forward=fwd))
     return now
 
 
@@ -94,3 +96,26 @@ def test_outputs_are_prepared_on_the_given_stream(calls):
     moe.moe_permute(s, x, idx, stream=st)
     made = [e for e in calls.log if e[0] == "made"]
     assert len(made) == 8 and all(e[2] is st for e in made) and ("ran", 0, 55) in calls.log
+
+
+def _layer(dev, T=4, d=64, E=8):
+    f = lambda sh, dt: Fake(dev, sh, dt)  # noqa: E731
+    i8, f32 = torch.int8, torch.float32
+    s = moe.MoeShape(T=T, d=d, E=E, k=2, H=16, wfmt=moe.WFMT_INT8)
+    return (s, f((T, d), torch.bfloat16), f((E, d), f32), f((E, 32, d), i8), f((E, d, 16), i8),
+            dict(s13=f((E, 32), f32), s2=f((E, d), f32)))
+
+
+def test_the_layer_and_the_router_run_on_their_tensors_device(calls):
+    s, x, wr, w13, w2, scales = _layer("cuda:1")
+    moe.moe_forward(s, x, wr, w13, w2, **scales)
+    moe.moe_route(s, x, wr)
+    moe.moe_route_from_logits(s, Fake("cuda:1", (4, 8), torch.float32))
+    assert [e for e in calls.log if e[0] == "ran"] == [("ran", 1, 101)] * 3
+    assert all(e[1] == 1 for e in calls.log) and calls.dev == 0
+    other = Fake("cuda:0", wr.shape, wr.dtype)
+    for call in (lambda: moe.moe_forward(s, x, other, w13, w2, **scales), lambda: moe.moe_route(s, x, other),
+                 lambda: moe.moe_forward(s, x, wr, w13, w2, s13=Fake("cuda:0", (8, 32), torch.float32), s2=scales["s2"])):
+        with pytest.raises(ValueError, match="cuda:0"):
+            call()
+    assert len([e for e in calls.log if e[0] == "ran"]) == 3
