@@ -5,9 +5,11 @@
 // infinity or a NaN gets that as its scale, so what is computed from it is not finite either.
 //
 // q is computed as fma(x, r, 1.5 2^23) with r = 127 / m rounded up: the sum's low byte is rint(x r).  For bf16 rows
-// this is exactly rint(127 x / m): with 8-bit significands a quotient that is no tie lies at least 1/510 away from
-// every tie, far more than the 2^-17 that r's rounding moves it; of the ties, those with 127 / m a power of two are
-// exact, and the others all have |x| = m / 2, where the quotient 63.5 rounds to 64 and r >= 127 / m keeps it there.
+// this is exactly rint(127 x / m).  r is less than 2^-23 of itself too large, which moves a quotient Q = 127 x / m by
+// less than 2^-23 Q.  With x = X 2^a and m = M 2^(a + s), X and M integers below 256, Q's distance from a tie n + 1/2 is
+// |254 X - (2n + 1) M 2^s| / (2 M 2^s): when it is not zero, at least 1 / (2 M 2^s) = Q / (254 X), about 2^-16 Q.  Of the
+// ties, those with 127 / m a power of two are exact; in the others 127 divides 2n + 1, so |x| = m / 2, where the quotient
+// 63.5 rounds to 64 and r >= 127 / m keeps it there.
 // (For fp32 rows a quotient within 2^-16 of a tie may go either way.)
 // The pass is bound by HBM: the row stays in registers between the maximum and the codes (131072 bf16 rows of 768: 48 us,
 // 6.3 TB/s).

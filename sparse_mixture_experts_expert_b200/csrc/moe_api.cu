@@ -726,6 +726,12 @@ static int launch_i8_t(const CUtensorMap& ta, const CUtensorMap& taf, const CUte
 }
 
 // out[R, N] bf16 = epilogue(codes A[R, K] . codes B_g^T) with row scales a_scale and channel scales b_scale.
+// Tiles are chosen by the bf16 products' rules.  CTA pairs from 192 rows a group on, a pair / single CTAs in us (rows over
+// experts, width x hidden): gate/up 131072 over 192, 768 x 512: 108 / 110; 65536 over 64, 1024 x 2048: 241 / 247; 20000
+// over 16, 2048 x 1024: 64 / 69; 8192 in one, 7168 x 4096: 287 / 329; down 67 / 81, 110 / 118, 40 / 45, 156 / 174.  About
+// 500 rows a group leave much of a 256-row tile empty, and short groups lose there: gate/up 16384 over 32, 768 x 4096:
+// SwiGLU 111 / 112, GeGLU 123 / 120, down 56 / 52; 4096 over 8, 4096 x 1536: 52 / 48 and 29 / 28; 2000 over 8, 7168 x 2048:
+// 71 / 62 and 33 / 38.
 static int int8_gemm(int mode, const void* A, const float* a_scale, long long R, int K, const void* B,
                      const float* b_scale, int n_groups, int b_rows, int up_row0, int N, const int32_t* gstart,
                      const int32_t* grows, void* out, cudaStream_t st, bool allow_pair) {
