@@ -158,6 +158,8 @@ def _want(t, dtype, shape, name):
 
 def _holds(t, dtype, n, name, more=True):
     """t holds the n values that are read or written from its first on (more: it may hold others behind them)."""
+    if t is None:
+        raise ValueError(f"{name}: missing")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.numel() < n or (t.numel() > n and not more):

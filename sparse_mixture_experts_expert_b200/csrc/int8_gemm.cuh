@@ -17,10 +17,10 @@
 // in packed fp32 pairs, and no access to global memory between a tile's MMAs and its stores.  Pair tiles store by TMA,
 // others straight from the registers in whole 32-byte sectors.
 // Measured (B200): one dense group of 8192 rows, 7168 -> 2 x 4096: 263 us, 3660 TOP/s.  16384 rows over 32 experts,
-// GeGLU 768 -> 4096: gate/up 119 us (1730 TOP/s; 117 us with a tail formula two terms shorter), down 55 us (1870 TOP/s);
+// GeGLU 768 -> 4096: gate/up 116 us (1780 TOP/s; 113 us with a tail formula two terms shorter), down 54 us (1890 TOP/s);
 // on another GPU at 1.58 GHz 125 and 57 us, tensor pipe 50 and 54% busy, DRAM 31 and 39%.  There the groups cost the
 // rest: a third of the 256-row tiles is nearly empty, and 300 MB of weights come from HBM (one dense group of that
-// shape: 74 and 40 us).  Keeping the A tile in shared memory for four column tiles (half the operand bytes) left the
+// shape: 87 and 40 us).  Keeping the A tile in shared memory for four column tiles (half the operand bytes) left the
 // gate/up kernel at 121 us against 118.
 // 64 rows over 48 experts of 7168 x 2048: 159 and 85 us, the weights at 6.4 TB/s.
 // Row tiles of at most 64 rows load them in boxes of 32, no more than the group has: with a handful of rows an expert
