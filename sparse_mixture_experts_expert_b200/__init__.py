@@ -137,13 +137,16 @@ def _ptr(t):
 
 # The current stream's handle without a Stream object around it (0.1 us a call instead of 3.2), where torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# torch.cuda.current_device and is_current_stream_capturing without their checks that CUDA is up (0.3 us a call).
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -170,20 +173,18 @@ _HERE_CTX = contextlib.nullcontext()
 
 
 def _on(stream, *tensors):
-    """Context of a call on these tensors: their one device current, and `stream` (or that device's current stream)
-    the one that outputs and scratch are allocated for."""
-    dev = None
+    """Context of a call on these tensors (the first is not None): their one device current, and `stream` (or that
+    device's current stream) the one that outputs and scratch are allocated for."""
+    first = tensors[0]
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("device tensor expected")
     for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-            if dev.type != "cuda":
-                raise ValueError("device tensor expected")
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    if stream is None and dev.index == torch.cuda.current_device():
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    if stream is None and index == _device():
         return _HERE_CTX
+    dev = first.device
     if stream is not None and stream.device != dev:
         raise ValueError(f"stream of {stream.device}, tensors on {dev}")
     ctx = contextlib.ExitStack()
@@ -214,26 +215,27 @@ def workspace(shape: MoeShape, device=None) -> torch.Tensor:
     host thread on one stream it is kept and grown on demand.  A call on another stream, from another thread or under
     graph capture gets a buffer of its own, allocated for that stream (or by the graph): scratch is never shared by
     calls that may overlap."""
-    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    index = dev.index if dev.index is not None else torch.cuda.current_device()
-    need = max(moe_workspace_size(shape), 256)
-    with _HERE_CTX if index == torch.cuda.current_device() else torch.cuda.device(index):
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(need, dtype=torch.uint8, device=dev)
-        handle = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
-        held = _held.of.get(index)
-        if held is None or held[0] != handle or held[1].numel() < need:
-            held = (handle, torch.empty(need, dtype=torch.uint8, device=dev))
-            _held.of[index] = held
+    index = torch.device(device).index if device is not None else None
+    if index is None or index == _device():
+        return _scratch(shape)
+    with torch.cuda.device(index):
+        return _scratch(shape)
+
+
+def _scratch(shape: MoeShape, stream=None) -> torch.Tensor:
+    """workspace() on the current device, for a call on `stream` (None: the current one)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _scratch(shape)
+    need, index = max(moe_workspace_size(shape), 256), _device()
+    if _capturing():
+        return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+    handle = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+    held = _held.of.get(index)
+    if held is None or held[0] != handle or held[1].numel() < need:
+        held = (handle, torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index)))
+        _held.of[index] = held
     return held[1]
-
-
-def _scratch(shape: MoeShape, dev, stream) -> torch.Tensor:
-    """workspace() for a call on `stream` (None: the current one)."""
-    if stream is None:
-        return workspace(shape, dev)
-    with torch.cuda.stream(stream):
-        return workspace(shape, dev)
 
 
 def moe_capacity(T: int, k: int, E: int, factor: float) -> int:
@@ -257,7 +259,7 @@ def moe_route(shape: MoeShape, x, w_router, bias=None, *, logits=False, aux=Fals
             out["aux_f"] = torch.empty(E, dtype=torch.float32, device=dev)
             out["aux_p"] = torch.empty(E, dtype=torch.float32, device=dev)
             out["aux"] = torch.empty(1, dtype=torch.float32, device=dev)
-        ws = ws if ws is not None else _scratch(shape, dev, stream)
+        ws = ws if ws is not None else _scratch(shape, stream)
         rc = _L().moe_route(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(out.get("logits")),
                             _ptr(out["topk_idx"]), _ptr(out["topk_w"]), _ptr(out["counts"]), _ptr(out.get("aux_f")),
                             _ptr(out.get("aux_p")), _ptr(out.get("aux")), _ptr(ws), ws.numel(), _stream(stream))
@@ -277,7 +279,7 @@ def moe_route_from_logits(shape: MoeShape, logits, *, aux=False, ws=None, stream
             out["aux_f"] = torch.empty(E, dtype=torch.float32, device=dev)
             out["aux_p"] = torch.empty(E, dtype=torch.float32, device=dev)
             out["aux"] = torch.empty(1, dtype=torch.float32, device=dev)
-        ws = ws if ws is not None else _scratch(shape, dev, stream)
+        ws = ws if ws is not None else _scratch(shape, stream)
         rc = _L().moe_route_from_logits(ctypes.byref(shape), _ptr(logits), _ptr(out["topk_idx"]), _ptr(out["topk_w"]),
                                         _ptr(out["counts"]), _ptr(out.get("aux_f")), _ptr(out.get("aux_p")),
                                         _ptr(out.get("aux")), _ptr(ws), ws.numel(), _stream(stream))
@@ -310,7 +312,7 @@ def moe_permute(shape: MoeShape, x, topk_idx, *, ws=None, stream=None, out=None)
             _want(out["x_perm"], torch.bfloat16, (shape.R, d), "out['x_perm']")
             _want(out["row_src"], torch.int32, (shape.R,), "out['row_src']")
             _want(out["slot_pos"], torch.int32, (T, k), "out['slot_pos']")
-        ws = ws if ws is not None else workspace(shape, x.device)
+        ws = ws if ws is not None else _scratch(shape)
         rc = _L().moe_permute(ctypes.byref(shape), _ptr(x), _ptr(topk_idx), _ptr(out["slot_pos"]),
                               _ptr(out["drop_mask"]), _ptr(out["counts"]), _ptr(out["kept"]), _ptr(out["offsets"]),
                               _ptr(out["row_src"]), _ptr(out["x_perm"]), _ptr(ws), ws.numel(), _stream())
@@ -415,7 +417,7 @@ def moe_forward(shape: MoeShape, x, w_router, w13, w2, *, bias=None, s13=None, s
             r.update(aux_f=torch.empty(E, dtype=torch.float32, device=dev),
                      aux_p=torch.empty(E, dtype=torch.float32, device=dev),
                      aux=torch.empty(1, dtype=torch.float32, device=dev))
-        ws = ws if ws is not None else _scratch(shape, dev, stream)
+        ws = ws if ws is not None else _scratch(shape, stream)
         rc = _L().moe_forward(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w13), _ptr(s13), _ptr(w2),
                               _ptr(s2), _ptr(w13_sh), _ptr(s13_sh), _ptr(w2_sh), _ptr(s2_sh), _ptr(out),
                               _ptr(r.get("topk_idx")), _ptr(r.get("topk_w")), _ptr(r.get("counts")),

@@ -19,6 +19,9 @@ class Fake:
     def is_contiguous(self):
         return True
 
+    def get_device(self):
+        return self.device.index
+
     def data_ptr(self):
         return 4096
 
@@ -44,10 +47,10 @@ def calls(monkeypatch):
         old, now.stream = now.stream, st
         yield
         now.stream = old
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: now.dev)
+    monkeypatch.setattr(moe, "_device", lambda: now.dev)
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "stream", on_stream)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(moe, "_capturing", lambda: False)
     monkeypatch.setattr(moe, "_raw_stream", lambda dev: 100 + dev if now.stream is None else now.stream.cuda_stream)
     made = lambda *sh, dtype=None, device=None: (now.log.append(("made", now.dev, now.stream)),     # noqa: E731
                                                  Fake(device, sh, dtype))[1]

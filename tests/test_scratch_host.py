@@ -22,8 +22,8 @@ def gpu(monkeypatch):
         state.kept.append(real_empty(*sh, **kw))
         return state.kept[-1]
     monkeypatch.setattr(torch, "empty", empty)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.capturing)
+    monkeypatch.setattr(moe, "_device", lambda: 0)
+    monkeypatch.setattr(moe, "_capturing", lambda: state.capturing)
     monkeypatch.setattr(moe, "_raw_stream", lambda dev: state.stream)
     monkeypatch.setattr(moe, "_held", type(moe._held)())
     monkeypatch.setattr(moe, "moe_workspace_size", lambda shape: 1024 * shape.T)
