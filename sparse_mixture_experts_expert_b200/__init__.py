@@ -194,6 +194,11 @@ def _on(stream, *tensors):
     return ctx
 
 
+def _given(stream):
+    """Context in which `stream` is the current one (None: as it is)."""
+    return _HERE_CTX if stream is None else torch.cuda.stream(stream)
+
+
 class _Held(threading.local):
     """The scratch that workspace() keeps: device index -> (stream handle, buffer), one of each host thread."""
 
@@ -225,7 +230,7 @@ def workspace(shape: MoeShape, device=None) -> torch.Tensor:
 def _scratch(shape: MoeShape, stream=None) -> torch.Tensor:
     """workspace() on the current device, for a call on `stream` (None: the current one)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _given(stream):
             return _scratch(shape)
     need, index = max(moe_workspace_size(shape), 256), _device()
     if _capturing():
@@ -446,15 +451,16 @@ def _backward(shape, x, w_router, w13, w2, dout, bias, w13t, w2t, w13_sh, w2_sh,
     T, d, E, H, Hs = shape.T, shape.d, shape.E, shape.H, shape.H_s
     _want(x, torch.bfloat16, (T, d), "x")
     _want(dout, torch.bfloat16, (T, d), "dout")
-    w13t = w13t if w13t is not None else moe_transpose_experts(w13, stream=stream)
-    w2t = w2t if w2t is not None else moe_transpose_experts(w2, stream=stream)
-    if Hs:
-        w13t_sh = w13t_sh if w13t_sh is not None else moe_transpose_experts(w13_sh, stream=stream)
-        w2t_sh = w2t_sh if w2t_sh is not None else moe_transpose_experts(w2_sh, stream=stream)
-    if ws is None:
-        n = ctypes.c_size_t(0)
-        _check(_L().moe_backward_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "moe_backward_workspace_size")
-        ws = torch.empty(int(n.value), dtype=torch.uint8, device=x.device)
+    with _given(stream):   # scratch and transposed copies live for this call on its stream
+        w13t = w13t if w13t is not None else moe_transpose_experts(w13)
+        w2t = w2t if w2t is not None else moe_transpose_experts(w2)
+        if Hs:
+            w13t_sh = w13t_sh if w13t_sh is not None else moe_transpose_experts(w13_sh)
+            w2t_sh = w2t_sh if w2t_sh is not None else moe_transpose_experts(w2_sh)
+        if ws is None:
+            n = ctypes.c_size_t(0)
+            _check(_L().moe_backward_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "moe_backward_workspace_size")
+            ws = torch.empty(int(n.value), dtype=torch.uint8, device=x.device)
     f32 = dict(dtype=torch.float32, device=x.device)
     g = dict(dx=torch.empty(T, d, **f32))
     head = [ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w13), _ptr(w13t), _ptr(w2t),
@@ -505,7 +511,8 @@ def moe_route_tree(shape: MoeShape, branch: int, levels: int, x, w_tree, bias_tr
         nb = ctypes.c_size_t(0)
         _check(_L().moe_route_tree_workspace_size(ctypes.byref(shape), branch, levels, ctypes.byref(nb)),
                "moe_route_tree_workspace_size")
-        ws = torch.empty(int(nb.value), dtype=torch.uint8, device=dev)
+        with _given(stream):
+            ws = torch.empty(int(nb.value), dtype=torch.uint8, device=dev)
     out = dict(topk_idx=torch.empty(T, k, dtype=torch.int32, device=dev),
                topk_w=torch.empty(T, k, dtype=torch.float32, device=dev),
                counts=torch.empty(E, dtype=torch.int32, device=dev) if counts else None,

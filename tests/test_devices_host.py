@@ -122,3 +122,29 @@ def test_the_layer_and_the_router_run_on_their_tensors_device(calls):
         with pytest.raises(ValueError, match="cuda:0"):
             call()
     assert len([e for e in calls.log if e[0] == "ran"]) == 3
+
+
+def test_scratch_that_a_call_frees_belongs_to_the_given_stream(calls, monkeypatch):
+    # freed at the end of the call: memory of the current stream could be handed out while the call still runs
+    def size(*a):
+        a[-1]._obj.value = 1024
+        return 0
+    ran = lambda *a: 0  # noqa: E731
+    monkeypatch.setattr(moe, "_L", lambda: SimpleNamespace(
+        moe_backward_workspace_size=size, moe_route_tree_workspace_size=size, moe_transpose_experts=ran, moe_backward=ran,
+        moe_backward_x=ran, moe_route_tree=ran))
+    st = SimpleNamespace(device=torch.device("cuda:0"), cuda_stream=55)
+    f = lambda *sh, dt=torch.bfloat16: Fake("cuda:0", sh, dt)  # noqa: E731
+    s = moe.MoeShape(T=4, d=64, E=8, k=2, H=16)
+    made = []
+    monkeypatch.setattr(torch, "empty", lambda *sh, dtype=None, device=None: (made.append((dtype, calls.stream)),
+                                                                             f(*sh, dt=dtype))[1])
+    args = (s, f(4, 64), f(8, 64, dt=torch.float32), f(8, 32, 64), f(8, 64, 16), f(4, 64))
+    for call in (moe.moe_backward, moe.moe_backward_x):
+        made.clear()
+        call(*args, stream=st)
+        temp = [e for e in made if e[0] in (torch.uint8, torch.bfloat16)]      # workspace and transposed weights
+        assert len(temp) == 3 and all(e[1] is st for e in temp)
+    made.clear()
+    moe.moe_route_tree(moe.MoeShape(T=4, d=64, E=64, k=2, H=16), 8, 2, f(4, 64), f(16, 64, dt=torch.float32), stream=st)
+    assert [e[1] for e in made if e[0] == torch.uint8] == [st]
